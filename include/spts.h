@@ -315,6 +315,112 @@ SPTS_API spts_status spts_select_sequential(const float *s_a, const float *s_b, 
 SPTS_API size_t spts_select_sequential_workspace(int64_t Nc);
 
 /* ---------------------------------------------------------------------- */
+/* The paged key/value cache a prefill leaves: fill, attend, evict          */
+/* ---------------------------------------------------------------------- */
+
+/* K and V rows of B sequences in pages of page_size slots.  Slot t of
+ * sequence b is row t % page_size of page page_table[b, t / page_size].
+ *   k_pages, v_pages  [num_pages, page_size, Hkv, d] bf16, consecutive pages
+ *                     page_stride elements apart (0: page_size * Hkv * d)
+ *   page_table        [B, max_pages] int32, rows table_stride entries apart
+ *                     (0: max_pages); only the entries of pages that hold a
+ *                     slot below the sequence's length are read
+ *   seq_lens          [B] int32: cached tokens of each sequence, the new
+ *                     tokens of the call included
+ * Slots are in the order of the tokens; K rows carry their RoPE, so after an
+ * eviction slot numbers need not be positions.  A page must not belong to two
+ * sequences of a call that writes to it.
+ * The lengths, offsets and page numbers live on the device: a length outside
+ * [0, max_pages * page_size], an offset outside [0, T] or below the one
+ * before it, or a page number outside [0, num_pages) raises the INVALID flag
+ * of ws; nothing is read or written out of bounds, and the results of the
+ * sequences concerned are unspecified.
+ * Limits: dtype BF16; d in {64, 128}; 1 <= Hq / Hkv <= 128; page_size in
+ * {16, 32, 64, 128, 256}; 1 <= B <= 1024; max_pages >= 1 with
+ * max_pages * page_size <= 2^30; page_stride % 8 == 0. */
+typedef struct {
+  void *k_pages, *v_pages;
+  int64_t num_pages, page_stride;
+  int page_size;
+  int B;
+  const int32_t *page_table;
+  int max_pages;
+  int64_t table_stride;
+  const int32_t *seq_lens;
+} spts_paged_cache;
+
+/* Writes the K and V rows of new tokens to the last slots of their
+ * sequences: with n = cu_new[b+1] - cu_new[b], row cu_new[b] + i goes to slot
+ * seq_lens[b] - n + i of sequence b (n > seq_lens[b] raises the INVALID flag
+ * and the rows without a slot are skipped).
+ *   k_new, v_new  [T, Hkv, d] bf16, rows k_stride / v_stride elements apart
+ *                 (multiples of 8, 0: Hkv * d)
+ *   cu_new        [B + 1] int32 ascending from 0; rows from cu_new[B] on are
+ *                 padding and not read
+ *   pos           [T] int32 positions >= 0 of the rotate-half RoPE applied to
+ *                 K (as spts_rope, rounded once to bf16), or NULL: K is
+ *                 stored as given
+ * ws: 256 bytes for the status word, or NULL.  a: Hkv, d and dtype are used. */
+SPTS_API spts_status spts_cache_append(const spts_attn_desc *a, const spts_paged_cache *c, const void *k_new,
+                                       int64_t k_stride, const void *v_new, int64_t v_stride,
+                                       const int32_t *cu_new, int64_t T, const int32_t *pos, double theta,
+                                       void *ws, spts_stream stream);
+
+/* Attention of new tokens over the cache: with n = cu_q[b+1] - cu_q[b] and
+ * L = seq_lens[b], query row cu_q[b] + i sees the slots t <= L - n + i of
+ * sequence b (its own token, which must be cached already, and all before it;
+ * n == 1 is a step of decoding, n == L a whole prompt).
+ *   q, o     [T, Hq, d] bf16, rows q_stride / o_stride elements apart
+ *            (multiples of 8, 0: Hq * d); rows from cu_q[B] on are not read
+ *            and left as they are
+ *   cu_q     [B + 1] int32 ascending from 0
+ *   lse      [T, Hq] fp32 out, or NULL: ln of the sum over the visible slots
+ *            of exp(scale * q . k) (-inf for a row that sees none)
+ *   weights  [B, Hs, w_stride] fp32 in/out, or NULL; Hs = Hkv or 1.
+ *            weights[b, g, t] += the softmax weight that slot t received,
+ *            summed over the sequence's new tokens and the query heads of KV
+ *            head g (all query heads with Hs = 1), in a fixed order
+ *            w_stride >= max_pages * page_size; slots from L on are left
+ * A row that sees no slot is written as 0.  Slots from L on may hold
+ * anything; a non-finite K or V row of a token reaches the rows that see it
+ * and may reach rows of the same call before it, but no other sequence. */
+SPTS_API spts_status spts_paged_attention(const spts_attn_desc *a, const spts_paged_cache *c, const void *q,
+                                          int64_t q_stride, const int32_t *cu_q, int64_t T, void *o,
+                                          int64_t o_stride, float *lse, float *weights, int Hs,
+                                          int64_t w_stride, void *ws, size_t ws_bytes, spts_stream stream);
+/* with_weights: whether `weights` will be given. */
+SPTS_API size_t spts_paged_attention_workspace(const spts_attn_desc *a, const spts_paged_cache *c, int64_t T,
+                                               int with_weights);
+
+/* Eviction by accumulated attention weight.  Every sequence longer than
+ * `keep` keeps `keep` of its tokens: the first `sink`, the last `recent` and,
+ * of the others, those of the largest weight (ties to the lower slot, -0
+ * counts as +0); shorter ones keep all.  The choice is made per KV head
+ * (Hs = Hkv) or once for all heads (Hs = 1).  The kept rows move, in order,
+ * to the slots 0, 1, ... of dst_table.
+ *   weights      [B, Hs, w_stride] fp32; finite below seq_lens[b]
+ *                (w_stride >= max_pages * page_size)
+ *   dst_table    [B, dst_max_pages] int32, rows dst_stride entries apart (0:
+ *                dst_max_pages), pages of the same k_pages / v_pages with room
+ *                for min(seq_lens[b], keep) slots.  Either disjoint from every
+ *                page the cache's own table names, or that same pointer:
+ *                then the cache is compacted in place
+ *   weights_out  [B, Hs, w_out_stride] fp32 out, disjoint from weights, or
+ *                weights itself; w_out_stride >= min(keep, max_pages *
+ *                page_size).  The kept tokens' weights, then zeros to the
+ *                end of the row
+ *   new_lens     [B] int32 out: min(seq_lens[b], keep); may be seq_lens
+ *   kept_idx     [B, Hs, keep] int32 out or NULL: the slots kept, ascending,
+ *                then -1
+ * Limits: keep >= 1, sink, recent >= 0, sink + recent <= keep. */
+SPTS_API spts_status spts_cache_evict(const spts_attn_desc *a, const spts_paged_cache *c, const float *weights,
+                                      int Hs, int64_t w_stride, int64_t keep, int64_t sink, int64_t recent,
+                                      const int32_t *dst_table, int dst_max_pages, int64_t dst_stride,
+                                      float *weights_out, int64_t w_out_stride, int32_t *new_lens,
+                                      int32_t *kept_idx, void *ws, size_t ws_bytes, spts_stream stream);
+SPTS_API size_t spts_cache_evict_workspace(const spts_paged_cache *c, int Hs, int64_t keep);
+
+/* ---------------------------------------------------------------------- */
 /* The composed layer (probe -> reduced MHA -> LTP -> reduced FFN)         */
 /* ---------------------------------------------------------------------- */
 

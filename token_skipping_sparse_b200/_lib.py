@@ -35,6 +35,8 @@ EXPORTS = (
     "spts_linear_workspace", "spts_inject_salience", "spts_layer_forward", "spts_layer_forward_workspace",
     "spts_msdp_forward", "spts_msdp_forward_workspace", "spts_schedule_forward", "spts_schedule_forward_workspace",
     "spts_layer_forward_bf16io", "spts_layer_forward_bf16io_workspace", "spts_debug_exp2_poly",
+    "spts_cache_append", "spts_paged_attention", "spts_paged_attention_workspace", "spts_cache_evict",
+    "spts_cache_evict_workspace",
 )
 
 
@@ -76,6 +78,12 @@ class LayerWeights(C.Structure):
 class LayerOutputs(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("s", "c", "f", "idx_attn", "idx_ffn", "o_sel", "h_attn", "k",
                                           "q_probe", "stage_events")]
+
+
+class PagedCache(C.Structure):
+    _fields_ = [("k_pages", C.c_void_p), ("v_pages", C.c_void_p), ("num_pages", C.c_int64),
+                ("page_stride", C.c_int64), ("page_size", C.c_int), ("B", C.c_int), ("page_table", C.c_void_p),
+                ("max_pages", C.c_int), ("table_stride", C.c_int64), ("seq_lens", C.c_void_p)]
 
 
 LAYER_STAGE_EVENTS = 16
@@ -137,6 +145,12 @@ _sig("spts_schedule_forward", i32, [C.POINTER(LayerDesc), C.POINTER(LayerWeights
                                     C.POINTER(C.c_int64), i32, i64, vp, vp, i64, C.POINTER(C.c_int64), vp, i64,
                                     C.POINTER(C.c_int64), vp, sz, vp])
 _sig("spts_schedule_forward_workspace", sz, [C.POINTER(LayerDesc), i64])
+PC = C.POINTER(PagedCache)
+_sig("spts_cache_append", i32, [AD, PC, vp, i64, vp, i64, vp, i64, vp, f64, vp, vp])
+_sig("spts_paged_attention", i32, [AD, PC, vp, i64, vp, i64, vp, i64, vp, vp, i32, i64, vp, sz, vp])
+_sig("spts_paged_attention_workspace", sz, [AD, PC, i64, i32])
+_sig("spts_cache_evict", i32, [AD, PC, vp, i32, i64, i64, i64, i64, vp, i32, i64, vp, i64, vp, vp, vp, sz, vp])
+_sig("spts_cache_evict_workspace", sz, [PC, i32, i64])
 
 
 # ---------------------------------------------------------------- helpers
@@ -367,6 +381,194 @@ def spts_inject_salience(k, q_probe, rows, shift):
     check(lib.spts_inject_salience(ptr(k), Nc, ptr(q_probe), P, Hq, Hkv, d, ptr(rows), rows.shape[0], shift,
                                    stream_ptr()))
     return k
+
+
+# ---------------------------------------------------------------- the paged key/value cache
+def _want(t, dtype, dims, device, what):
+    """What the library cannot see behind a pointer: type, rank, device."""
+    if t.dtype != dtype or t.dim() != dims or t.device != device:
+        raise ValueError(f"{what}: need a {dims}-dimensional {dtype} tensor on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _inner(t, what):
+    """Row stride of packed tokens whose heads lie as in a contiguous tensor."""
+    _, H, d = t.shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+        raise ValueError(f"{what}: heads and columns must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else H * d
+
+
+def _row_stride(t, what):
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: entries of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[-1]
+
+
+def _score_stride(t, what):
+    """Stride between the rows [b, hs] of a weights tensor."""
+    B, Hs, n = t.shape
+    row = t.stride(1) if Hs > 1 else t.stride(0) if B > 1 else n
+    if (n > 1 and t.stride(2) != 1) or (B > 1 and t.stride(0) != Hs * row):
+        raise ValueError(f"{what}: need evenly spaced rows of contiguous entries")
+    return row
+
+
+def _paged(k_pages, v_pages, page_table, seq_lens):
+    dev = k_pages.device
+    _want(k_pages, torch.bfloat16, 4, dev, "k_pages")
+    _want(v_pages, torch.bfloat16, 4, dev, "v_pages")
+    _want(page_table, torch.int32, 2, dev, "page_table")
+    _want(seq_lens, torch.int32, 1, dev, "seq_lens")
+    n, page, Hkv, d = k_pages.shape
+    inner = (Hkv * d, d, 1)
+    if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() or \
+            any(k > 1 and s != want for k, s, want in zip(k_pages.shape[1:], k_pages.stride()[1:], inner)):
+        raise ValueError("k_pages and v_pages must be alike, and contiguous inside a page")
+    B = seq_lens.shape[0]
+    if page_table.shape[0] != B or (B > 1 and seq_lens.stride(0) != 1):
+        raise ValueError("page_table and seq_lens need one row and one contiguous entry per sequence")
+    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), n, k_pages.stride(0) if n > 1 else 0, page, B,
+                      page_table.data_ptr(), page_table.shape[1], _row_stride(page_table, "page_table"),
+                      seq_lens.data_ptr())
+
+
+def _offsets(cu, B, dev, what):
+    _want(cu, torch.int32, 1, dev, what)
+    if cu.shape[0] != B + 1 or cu.stride(0) != 1:
+        raise ValueError(f"{what}: need B + 1 contiguous offsets")
+    return ptr(cu)
+
+
+def _own_ws(ws, nbytes, dev):
+    """The caller's workspace, or the cached one.  A captured graph would keep
+    the cached one's address after a larger call has replaced it."""
+    if ws is not None:
+        return _want(ws, torch.uint8, 1, dev, "ws")
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError("pass a workspace of your own (ws) while a graph is captured")
+    return workspace(nbytes, dev)
+
+
+def _on_device(fn):
+    """Runs a cache call with the device of its first tensor current, so that
+    its launches, stream and workspace are that device's."""
+    import functools
+
+    @functools.wraps(fn)
+    def call(first, *args, **kw):
+        if first.device.type != "cuda":
+            raise ValueError(f"{fn.__name__}: tensors must be on a CUDA device, got {first.device}")
+        if first.device.index == torch.cuda.current_device():
+            return fn(first, *args, **kw)
+        with torch.cuda.device(first.device):
+            return fn(first, *args, **kw)
+    return call
+
+
+@_on_device
+def spts_cache_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, cu_new, pos=None, theta=500000.0, ws=None):
+    """Writes packed new tokens' K (turned by RoPE at pos, if given) and V [T, Hkv, d] to the last slots of their
+    sequences; seq_lens counts them already."""
+    dev = k_new.device
+    c = _paged(_want(k_pages, torch.bfloat16, 4, dev, "k_pages"), v_pages, page_table, seq_lens)
+    T, Hkv, d = _want(k_new, torch.bfloat16, 3, dev, "k_new").shape
+    if _want(v_new, torch.bfloat16, 3, dev, "v_new").shape != k_new.shape or (Hkv, d) != tuple(k_pages.shape[2:]):
+        raise ValueError("k_new, v_new and the pages must agree in heads and head dim")
+    if pos is not None and (_want(pos, torch.int32, 1, dev, "pos").shape[0] != T or (T > 1 and pos.stride(0) != 1)):
+        raise ValueError("pos: need one contiguous position per new token")
+    a = AttnDesc(BF16, Hkv, Hkv, d, 0.0)
+    ws = _own_ws(ws, 256, dev)
+    check(lib.spts_cache_append(C.byref(a), C.byref(c), ptr(k_new), _inner(k_new, "k_new"), ptr(v_new),
+                                _inner(v_new, "v_new"), _offsets(cu_new, c.B, dev, "cu_new"), T, ptr(pos), theta,
+                                ptr(ws), stream_ptr()))
+
+
+def _weights_arg(weights, c, Hkv, dev, what):
+    B, Hs, n = _want(weights, torch.float32, 3, dev, what).shape
+    if B != c.B or Hs not in (1, Hkv):
+        raise ValueError(f"{what}: need [B, 1 or Hkv, slots]")
+    return Hs, _score_stride(weights, what), n
+
+
+def spts_paged_attention_workspace(q, k_pages, v_pages, page_table, seq_lens, weights=False):
+    """Bytes of workspace that spts_paged_attention needs for these arguments."""
+    T, Hq, d = q.shape
+    a = AttnDesc(BF16, Hq, k_pages.shape[2], d, 0.0)
+    c = _paged(k_pages, v_pages, page_table, seq_lens)
+    return int(lib.spts_paged_attention_workspace(C.byref(a), C.byref(c), T, 1 if weights else 0))
+
+
+@_on_device
+def spts_paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_q, scale=None, out=None, lse=False,
+                         weights=None, ws=None):
+    """Attention of packed new tokens q [T, Hq, d] over the paged cache, causal inside each sequence.
+    Returns o [T, Hq, d], with lse=True (o, lse [T, Hq]); `weights` [B, Hkv or 1, slots] is added to in place."""
+    dev = q.device
+    c = _paged(_want(k_pages, torch.bfloat16, 4, dev, "k_pages"), v_pages, page_table, seq_lens)
+    T, Hq, d = _want(q, torch.bfloat16, 3, dev, "q").shape
+    Hkv = k_pages.shape[2]
+    if d != k_pages.shape[3]:
+        raise ValueError("q and the pages must agree in head dim")
+    a = AttnDesc(BF16, Hq, Hkv, d, 0.0 if scale is None else float(scale))
+    if out is None:
+        o = torch.empty(T, Hq, d, dtype=torch.bfloat16, device=dev)
+    else:
+        o = out
+        if _want(o, torch.bfloat16, 3, dev, "out").shape != q.shape:
+            raise ValueError("out: need q's shape")
+    e = torch.empty(T, Hq, dtype=torch.float32, device=dev) if lse else None
+    Hs = stride = 0
+    if weights is not None:
+        Hs, stride, n = _weights_arg(weights, c, Hkv, dev, "weights")
+        if n < c.max_pages * c.page_size:
+            raise ValueError("weights: need a slot for every slot of a page table row")
+    ws = _own_ws(ws, lib.spts_paged_attention_workspace(C.byref(a), C.byref(c), T, 0 if weights is None else 1), dev)
+    check(lib.spts_paged_attention(C.byref(a), C.byref(c), ptr(q), _inner(q, "q"), _offsets(cu_q, c.B, dev, "cu_q"), T,
+                                   ptr(o), _inner(o, "out"), ptr(e), ptr(weights), Hs, stride, ptr(ws), ws.numel(),
+                                   stream_ptr()))
+    return (o, e) if lse else o
+
+
+def spts_cache_evict_workspace(k_pages, v_pages, page_table, seq_lens, weights, keep):
+    """Bytes of workspace that spts_cache_evict needs for these arguments."""
+    c = _paged(k_pages, v_pages, page_table, seq_lens)
+    return int(lib.spts_cache_evict_workspace(C.byref(c), weights.shape[1], keep))
+
+
+@_on_device
+def spts_cache_evict(k_pages, v_pages, page_table, seq_lens, weights, keep, sink=0, recent=0, dst_table=None,
+                     weights_out=None, new_lens=None, kept=False, ws=None):
+    """Keeps `keep` tokens of every longer sequence by accumulated weight.  With dst_table the kept rows go to its
+    pages, without it the cache and (unless weights_out is given) the weights are compacted in place.
+    Returns (new_lens, weights_out), with kept=True also the kept slots [B, Hs, keep] (-1 behind the last)."""
+    dev = k_pages.device
+    c = _paged(k_pages, v_pages, page_table, seq_lens)
+    Hkv, d = k_pages.shape[2:]
+    Hs, stride, n = _weights_arg(weights, c, Hkv, dev, "weights")
+    if n < c.max_pages * c.page_size:
+        raise ValueError("weights: need a slot for every slot of a page table row")
+    dst = page_table if dst_table is None else _want(dst_table, torch.int32, 2, dev, "dst_table")
+    if dst.shape[0] != c.B:
+        raise ValueError("dst_table: need one row per sequence")
+    if weights_out is None:
+        weights_out = weights if dst_table is None else torch.empty(
+            c.B, Hs, dst.shape[1] * c.page_size, dtype=torch.float32, device=dev)
+    Ho, out_stride, m = _weights_arg(weights_out, c, Hkv, dev, "weights_out")
+    if Ho != Hs or m != out_stride:
+        raise ValueError("weights_out: need contiguous rows, as many as weights has")
+    if new_lens is None:
+        new_lens = torch.empty(c.B, dtype=torch.int32, device=dev)
+    elif _want(new_lens, torch.int32, 1, dev, "new_lens").shape[0] != c.B or (c.B > 1 and new_lens.stride(0) != 1):
+        raise ValueError("new_lens: need one contiguous entry per sequence")
+    idx = torch.empty(c.B, Hs, keep, dtype=torch.int32, device=dev) if kept else None
+    a = AttnDesc(BF16, Hkv, Hkv, d, 0.0)
+    ws = _own_ws(ws, lib.spts_cache_evict_workspace(C.byref(c), Hs, keep), dev)
+    check(lib.spts_cache_evict(C.byref(a), C.byref(c), ptr(weights), Hs, stride, keep, sink, recent, ptr(dst),
+                               dst.shape[1], _row_stride(dst, "dst_table"), ptr(weights_out), out_stride,
+                               ptr(new_lens), ptr(idx), ptr(ws), ws.numel(), stream_ptr()))
+    return (new_lens, weights_out, idx) if kept else (new_lens, weights_out)
 
 
 # ---------------------------------------------------------------- the composed layer
