@@ -381,6 +381,8 @@ SPTS_API spts_status spts_cache_append(const spts_attn_desc *a, const spts_paged
  *            summed over the sequence's new tokens and the query heads of KV
  *            head g (all query heads with Hs = 1), in a fixed order
  *            w_stride >= max_pages * page_size; slots from L on are left
+ * The same call gives the same bits every time; the last bits of a sequence's
+ * rows may depend on the lengths of the others (where the work is divided).
  * A row that sees no slot is written as 0.  Slots from L on may hold
  * anything; a non-finite K or V row of a token reaches the rows that see it
  * and may reach rows of the same call before it, but no other sequence. */

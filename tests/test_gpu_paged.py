@@ -317,7 +317,7 @@ def test_bad_device_values_are_flagged_and_reach_no_other_sequence(bad):
     lens, new = [100, 50, 70], [60, 20, 1]
     c = Cache(lens, 16, 2, 128, seed=27)
     cu, q = packed(new, 8, 128, 28)
-    clean = S.spts_paged_attention(q, *c.args(), i32(cu))
+    want = P.paged_attention(f64(q), c.np_k, c.np_v, c.rows, lens, cu)
     S.check_device_status()
     rows, sizes = [list(r) for r in c.rows], list(lens)
     if bad == "length":
@@ -336,8 +336,11 @@ def test_bad_device_values_are_flagged_and_reach_no_other_sequence(bad):
     o = S.spts_paged_attention(q, c.k, c.v, i32(rows), i32(sizes), i32(cu), weights=w)
     with pytest.raises(S.SptsError):
         S.check_device_status()
-    assert torch.equal(o[:60], clean[:60]) or bad == "descending"
-    assert torch.equal(o[80:], clean[80:]) or bad in ("offset", "descending")
+    # the other sequences are right within the bounds (their bits may move: the work is cut elsewhere)
+    err = 132 * 2.0 ** -23 * want["aqk"][..., None]
+    fine = np.abs(f64(o) - want["o"]) <= (U + 2 * err + 2.5e-4) * want["av"] + U * np.abs(want["o"])
+    assert np.all(fine[:60]) or bad == "descending"
+    assert np.all(fine[80:]) or bad in ("offset", "descending")
 
 
 def test_bad_pages_and_missing_slots_are_flagged_by_append_and_evict():

@@ -94,6 +94,7 @@ size_t spts_paged_attention_workspace(const spts_attn_desc *a, const spts_paged_
                                       int with_weights) {
   size_t b = kStatusBytes;
   if (a == nullptr || c == nullptr || T <= 0 || a->Hq <= 0) return b;
+  b += Carver::round(paged_attn_scratch_bytes(a->d));
   if (with_weights) b += Carver::round(static_cast<size_t>(T) * a->Hq * sizeof(float));  // lse
   return b;
 }
@@ -123,7 +124,7 @@ spts_status spts_paged_attention(const spts_attn_desc *a, const spts_paged_cache
   if (T == 0) return SPTS_OK;
   Carver cv(ws, ws_bytes);
   PagedAttnArgs args{q, q_stride, cu_q, T, a->Hq, 0.f, o, o_stride, lse, weights, weights ? Hs : 1, w_stride,
-                     cv.status()};
+                     cv.status(), cv.take(paged_attn_scratch_bytes(a->d))};
   args.scale = a->scale > 0.f ? a->scale : 1.0f / std::sqrt(static_cast<float>(a->d));
   if (weights) {
     float *own = static_cast<float *>(cv.take(static_cast<size_t>(T) * a->Hq * sizeof(float)));

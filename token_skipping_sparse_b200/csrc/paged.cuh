@@ -90,7 +90,9 @@ struct PagedAttnArgs {
   int Hs;
   int64_t w_stride;
   uint32_t *status;
+  void *scratch;   // paged_attn_scratch_bytes(d)
 };
+size_t paged_attn_scratch_bytes(int d);
 spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, cudaStream_t s);
 
 struct EvictArgs {

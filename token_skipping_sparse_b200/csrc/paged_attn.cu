@@ -1,73 +1,759 @@
-// paged_attn.cu -- attention of new tokens over the paged cache.
+// paged_attn.cu -- attention of new tokens over the paged cache, on tcgen05.
+//
+// For query row (token i of a sequence, head h) and the slots t it sees,
+//   s_t = scale q . k_t,   o = sum_t 2^(s_t' - m) v_t / l,   l = sum_t 2^(s_t' - m)
+// with s' = s log2(e) and m the running maximum: one pass over the keys.
+//
+// A Q tile packs tq = 128 / G tokens x the G query heads of one KV head into
+// the 128 rows of an MMA; a unit is two such tiles (a window of 2 tq tokens)
+// and one KV head.  Bound by the tensor pipe and the exponentials when the
+// windows are full, by reading K and V once when there are few new tokens:
+// then a unit's rows are the same but most of them are padding, and what
+// counts is that K and V stream without a pause.  So one persistent CTA per
+// SM takes an equal share of all units' key slots, wherever the cuts fall
+// (paged_plan.hpp): one request over 128K slots and 64 requests of ragged
+// lengths both load every SM alike.  Units that a cut divides leave partial
+// results (unnormalised O, m, l) that the combine kernel joins, in order.
+//   warp 0      TMA: Q tiles, and K and V tiles of 128 slots into two rings;
+//               a tile is gathered from its pages, one box per page and 64
+//               columns, each issued by a lane of its own.  Pages past the
+//               sequence's last one (and bad page numbers) are loaded from
+//               outside the tensor: zeros;
+//   warp 1      MMA: S_x = Q_x K^T into TMEM, then O_x += P_x V with P_x read
+//               from TMEM; the loop runs across units without a drain;
+//   warp 2      zeroes the V rows behind the sequence's last slot in its last
+//               tile: they may hold anything, and 0 x NaN is NaN;
+//   warp 3      idle (completes the warpgroup for the register split);
+//   warps 4..7, 8..11  softmax, one thread per row, one warpgroup per S_x.
+// A unit with two tiles gives them to x = 0 and 1, and every K/V tile feeds
+// both.  A unit with one (n <= tq: decoding) gives the even key tiles to x = 0
+// and the odd ones to x = 1, with the same Q, and joins the two at the end:
+// the softmax of one key tile runs beside the MMAs of the next either way.
+// P is rounded to bf16 for the product with V (half a step, 2^-9 of each
+// weight); S, the maxima, the sums and O stay in fp32.
+// All barrier waits are bounded (see sm100.cuh).
 #include "host.hpp"
 #include "paged.cuh"
+#include "paged_plan.hpp"
+#include "sm100.cuh"
 
 namespace spts {
 namespace {
 
-// Sequence and place of packed row t.
-struct Row {
-  int b, i, n, L;
+constexpr int THREADS = 384;
+// setmaxnreg split: each SMSP holds one warp of warpgroup 0 and one softmax
+// warp of each tile: 88 + 2 x 208 = 3 x 168, the launch allocation.
+constexpr int REG_LOW = 88, REG_HIGH = 208;
+constexpr int BKV = PLAN_TILE;
+constexpr int CHUNK = 128 * 64 * 2;   // 128 rows of 64 bf16, 128-byte swizzle
+constexpr int MAX_SEQ = 1024;
+constexpr int SLOT_ROWS = 256;        // rows of a partial result: two Q tiles
+constexpr uint32_t TMEM_COLS = 512;   // S_0 [0,128), S_1 [128,256), O_0 from 256, O_1 from 384
+constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
+constexpr float LN2 = 0.69314718055994530942f;
+// One column pair in POLY_EVERY takes its exp2 from the FMA pipe when the
+// row sums serve the bf16 output alone; with lse or weights asked for, all
+// come from the MUFU pipe (2 ulp against 1e-4).
+constexpr int POLY_EVERY = 3;
+
+template <int D>
+struct Geometry {
+  static constexpr int CH = D / 64;                 // 64-column chunks of a row
+  static constexpr int TILE = CH * CHUNK;           // a Q, K or V tile
+  static constexpr int STAGES = D == 128 ? 2 : 4;   // per ring: 64 KB of K and of V in flight either way
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + 2 * TILE;
+  static constexpr int OFF_V = OFF_K + STAGES * TILE;
+  static constexpr int OFF_TAIL = OFF_V + STAGES * TILE;
 };
 
-__device__ __forceinline__ bool row_of(const PagedView &c, const int32_t *cu, int T, int t, uint32_t *status, Row &r) {
-  if (t >= __ldg(cu + c.B)) return false;
-  int lo = 0, hi = c.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid;
-    else hi = mid;
-  }
-  int first;
-  packed_span(cu, T, lo, status, first, r.n);
-  r.b = lo;
-  r.i = t - first;
-  r.L = paged_len(c, lo, status);
-  return r.i >= 0 && r.i < r.n;
+struct Walk {
+  PlanCursor cur;
+  PlanPiece pc;
+  int group, more;
+};
+
+struct Tail {  // shared memory behind the tiles
+  int64_t before[MAX_SEQ + 1];
+  PlanSeq seq[MAX_SEQ];
+  int first[MAX_SEQ];
+  float2 xchg[2][2][128];  // by turns: a warpgroup without a tile may be one piece ahead
+  uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
+  uint64_t v_fix[4];  // per stage, so that warp 2 cannot be two phases ahead of the MMA warp
+  uint64_t s_full[2], p_ready[4], o_done[2], o_free, x_full, drain;
+  Walk walk[12];
+  uint32_t tmem;
+  int abort_flag;
+};
+
+template <int D>
+constexpr size_t smem_bytes() {
+  return Geometry<D>::OFF_TAIL + sizeof(Tail);
 }
 
-// One warp per (row, query head): each lane holds d / 32 columns, one pass
-// over the visible slots with the running maximum and sum.
+struct Params {
+  PagedView c;
+  const int32_t *cu;
+  int T, Hq, G, tq;
+  int groups, group_heads;  // KV heads are taken in `groups` groups of at most group_heads
+  float scale_log2;
+  __nv_bfloat16 *o;
+  int64_t o_stride;
+  float *lse;
+  float *part_o;    // [groups][ctas][2][SLOT_ROWS][D]
+  float2 *part_ml;  // [groups][ctas][2][SLOT_ROWS]: running maximum (log2) and sum
+  PlanCut *cuts;    // [groups][ctas]
+  uint32_t *status;
+  uint64_t wait_ns;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Maxima that keep a NaN: a row that sees one comes out as NaN.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
+      "%6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ int heads_of(const Params &p, int group) {
+  return min(p.group_heads, p.c.Hkv - group * p.group_heads);
+}
+
+// The warp's next piece of this CTA's ranges, group after group, into its own
+// Walk (lane 0 steps, all lanes read).
+__device__ __forceinline__ bool walk_next(Walk &wk, const Tail &t, const Params &p) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    wk.more = 1;
+    while (wk.group < 0 || !plan_next(wk.cur, t.seq, p.c.B, 2 * p.tq, heads_of(p, wk.group), wk.pc)) {
+      if (++wk.group == p.groups) {
+        wk.more = 0;
+        break;
+      }
+      const int heads = heads_of(p, wk.group), r = blockIdx.x;
+      const int64_t total = t.before[p.c.B] * heads;
+      const int nr = plan_ranges(total, gridDim.x);
+      wk.cur.left = 0;
+      if (r < nr) {
+        const int64_t x = plan_cut(total, nr, r);
+        plan_open(wk.cur, t.seq, t.before, p.c.B, 2 * p.tq, heads, x, plan_cut(total, nr, r + 1) - x);
+      }
+    }
+  }
+  __syncwarp();
+  return wk.more != 0;
+}
+
+// Lengths and offsets of all sequences, and their costs added up.
+__device__ __forceinline__ void read_sequences(Tail &t, const Params &p) {
+  uint32_t *status = blockIdx.x == 0 ? p.status : nullptr;
+  for (int b = threadIdx.x; b < p.c.B; b += THREADS) {
+    int first, n;
+    packed_span(p.cu, p.T, b, status, first, n);
+    t.first[b] = first;
+    t.seq[b] = PlanSeq{n, paged_len(p.c, b, status)};
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int64_t run = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+      const int b = b0 + lane;
+      int64_t x = 0;
+      if (b < p.c.B) x = plan_cost(plan_base(t.seq[b]), plan_windows(t.seq[b].n, 2 * p.tq), 2 * p.tq);
+      int64_t incl = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (b < p.c.B) t.before[b] = run + incl - x;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) t.before[p.c.B] = run;
+  }
+  __syncthreads();
+}
+
+template <int D, bool EXACT>
+__global__ void __launch_bounds__(THREADS, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
+  using Gm = Geometry<D>;
+  constexpr int CH = Gm::CH, TILE = Gm::TILE, STAGES = Gm::STAGES;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *sQ = smem + Gm::OFF_Q, *sK = smem + Gm::OFF_K, *sV = smem + Gm::OFF_V;
+  Tail &t = *reinterpret_cast<Tail *>(smem + Gm::OFF_TAIL);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int *abort_flag = &t.abort_flag;
+
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) raise_status(p.status, SPTS_DEV_BADINDEX, 0x5Fu, smem_u32(smem));
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&t.q_full[x], 1);
+      mbar_init(&t.q_empty[x], 1);
+      mbar_init(&t.s_full[x], 1);
+      mbar_init(&t.p_ready[2 * x], 128);
+      mbar_init(&t.p_ready[2 * x + 1], 128);
+      mbar_init(&t.o_done[x], 1);
+    }
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&t.k_full[s], 1);
+      mbar_init(&t.k_empty[s], 1);
+      mbar_init(&t.v_full[s], 1);
+      mbar_init(&t.v_empty[s], 2);  // the MMA warp's commit and warp 2
+      mbar_init(&t.v_fix[s], 32);
+    }
+    mbar_init(&t.o_free, 256);
+    mbar_init(&t.x_full, 256);
+    mbar_init(&t.drain, 1);
+    t.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 12) t.walk[threadIdx.x].group = -1;
+  if (warp == 1) {
+    tmem_alloc(&t.tmem, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  read_sequences(t, p);  // ends with __syncthreads
+  tc_fence_after();
+  const uint32_t tmem = t.tmem;
+  Walk &wk = t.walk[warp];
+
+  if (warp == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
+    // ---------------- TMA, the whole warp: lane l issues box l of a tile
+    const int page = 1 << p.c.page_shift, rows = min(page, BKV), boxes = BKV / rows;
+    const bool mine = lane < boxes * CH;
+    const int box = lane / CH, ch = lane % CH;
+    int qc = 0, kc = 0;  // Q tiles and K/V tiles loaded so far
+    uint32_t k_issued = 0, k_par = 0, v_issued = 0, v_par = 0, q_issued = 0, q_par = 0;
+    bool ok = true;
+    auto wait_all = [&](uint64_t *bar, uint32_t parity, uint32_t where) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns, where));
+    };
+    while (ok && walk_next(wk, t, p)) {
+      const PlanPiece pc = wk.pc;
+      if (pc.t0 >= pc.t1) continue;
+      const PlanSeq s = t.seq[pc.b];
+      const int g = wk.group * p.group_heads + pc.g;
+      const int tok0 = pc.p * 2 * p.tq, tiles_q = s.n - tok0 > p.tq ? 2 : 1;
+      for (int x = 0; ok && x < tiles_q; ++x, ++qc) {
+        const int qs = qc & 1;
+        ok = wait_all(&t.q_empty[qs], ((qc >> 1) & 1) ^ 1, 0x51u);
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(&t.q_full[qs], p.tq * p.G * D * 2);
+          for (int i = 0; i < CH; ++i)
+            tma_load_3d(sQ + qs * TILE + i * CHUNK, &tmQ, &t.q_full[qs], i * 64, g * p.G,
+                        t.first[pc.b] + tok0 + x * p.tq);
+        }
+        if (ok) {
+          q_issued |= 1u << qs;
+          q_par = (q_par & ~(1u << qs)) | (((qc >> 1) & 1u) << qs);
+        }
+      }
+      // the page of this lane's box, one tile ahead; outside the tensor where there is none
+      auto page_of = [&](int j) -> int {
+        const int slot = j * BKV + box * rows;
+        if (!mine || slot >= s.L) return p.c.num_pages;
+        const int n = paged_page(p.c.table, p.c.table_stride, p.c.num_pages, pc.b, slot >> p.c.page_shift, p.status);
+        return n < 0 ? p.c.num_pages : n;
+      };
+      int next = page_of(pc.t0);
+      for (int j = pc.t0; ok && j < pc.t1; ++j, ++kc) {
+        const int st = kc % STAGES, at = next, row = (j * BKV) & (page - 1);
+        const uint32_t ph = (kc / STAGES) & 1;
+        if (j + 1 < pc.t1) next = page_of(j + 1);
+        const int off = st * TILE + ch * CHUNK + box * rows * 128;
+        ok = wait_all(&t.k_empty[st], ph ^ 1u, 0x52u);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&t.k_full[st], TILE);
+        __syncwarp();
+        if (mine) tma_load_4d(sK + off, &tmK, &t.k_full[st], ch * 64, g, row, at);
+        k_issued |= 1u << st;
+        k_par = (k_par & ~(1u << st)) | (ph << st);
+        ok = wait_all(&t.v_empty[st], ph ^ 1u, 0x53u);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&t.v_full[st], TILE);
+        __syncwarp();
+        if (mine) tma_load_4d(sV + off, &tmV, &t.v_full[st], ch * 64, g, row, at);
+        v_issued |= 1u << st;
+        v_par = (v_par & ~(1u << st)) | (ph << st);
+      }
+    }
+    if (*abort_flag && lane == 0) {
+      for (int i = 0; i < 2; ++i)
+        if (q_issued & (1u << i)) mbar_drain(&t.q_full[i], (q_par >> i) & 1u, p.status);
+      for (int i = 0; i < STAGES; ++i) {
+        if (k_issued & (1u << i)) mbar_drain(&t.k_full[i], (k_par >> i) & 1u, p.status);
+        if (v_issued & (1u << i)) mbar_drain(&t.v_full[i], (v_par >> i) & 1u, p.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
+    // ---------------- MMA: the whole warp runs the loop, one elected lane issues
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, BKV, 0, 0);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
+    auto wait_all = [&](uint64_t *bar, uint32_t parity, uint32_t where) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns, where));
+    };
+    int qc = 0, kc = 0, units = 0;
+    uint32_t fix_par = 0;  // per stage, the parity of its next mended tile
+    uint32_t used[2] = {0, 0};  // PVs issued per x
+    bool ok = true;
+    // S_x of the K tile in ring place `k` with the Q tile in place `q`, the q-th and k-th loaded
+    auto issue_s = [&](int x, int q, int k) -> bool {
+      const int st = k % STAGES, qs = q & 1;
+      if (!wait_all(&t.q_full[qs], (q >> 1) & 1, 0x54u)) return false;
+      if (!wait_all(&t.k_full[st], (k / STAGES) & 1, 0x55u)) return false;
+      tc_fence_after();
+      const uint32_t k_addr = smem_u32(sK + st * TILE), q_addr = smem_u32(sQ + qs * TILE);
+#pragma unroll
+      for (int kk = 0; kk < 4 * CH; ++kk) {
+        const uint64_t a = sdesc_k_sw128(q_addr + (kk >> 2) * CHUNK) + 2 * (kk & 3);
+        const uint64_t b = sdesc_k_sw128(k_addr + (kk >> 2) * CHUNK) + 2 * (kk & 3);
+        mma_bf16_ss_w(tmem + x * BKV, a, b, idesc_s, kk > 0);
+      }
+      tc_commit_w(&t.s_full[x]);
+      return true;
+    };
+    // O_x (+)= P_x V in two halves of 64 slots, each as soon as the softmax has stored it
+    auto issue_pv = [&](int x, int k, bool fresh) -> bool {
+      const int st = k % STAGES;
+      if (!wait_all(&t.v_full[st], (k / STAGES) & 1, 0x56u)) return false;
+      const uint32_t v_addr = smem_u32(sV + st * TILE);
+      for (int half = 0; half < 2; ++half) {
+        if (!wait_all(&t.p_ready[2 * x + half], used[x] & 1, 0x57u)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int kk = 4 * half + i;
+          mma_bf16_ts_w(tmem + 256 + x * 128, tmem + x * BKV + kk * 8, sdesc_mn_sw128(v_addr + kk * 16 * 128, CHUNK),
+                        idesc_pv, !(fresh && kk == 0));
+        }
+      }
+      tc_commit_w(&t.o_done[x]);
+      ++used[x];
+      return true;
+    };
+    while (ok && walk_next(wk, t, p)) {
+      const PlanPiece pc = wk.pc;
+      if (pc.t0 >= pc.t1) continue;
+      const PlanSeq s = t.seq[pc.b];
+      const int tok0 = pc.p * 2 * p.tq, n = pc.t1 - pc.t0;
+      const bool two = s.n - tok0 > p.tq;
+      // tiles of x = 0 when it has a Q tile of its own
+      const int n_a = two ? max(min((plan_visible(s, tok0 + p.tq) + BKV - 1) / BKV, pc.t1) - pc.t0, 0) : 0;
+      const int fix = (s.L & (BKV - 1)) ? s.L / BKV - pc.t0 : -1;  // the tile that warp 2 mends
+      bool fixed = fix < 0 || fix >= n;
+      bool free_ = false;
+      auto before_pv = [&](int i) -> bool {  // O free of the last unit, V of tile i mended
+        if (!free_) {
+          free_ = true;
+          if (!wait_all(&t.o_free, (units & 1) ^ 1, 0x58u)) return false;
+        }
+        if (!fixed && i == fix) {
+          fixed = true;
+          const int st = (kc + i) % STAGES;
+          if (!wait_all(&t.v_fix[st], (fix_par >> st) & 1u, 0x59u)) return false;
+          fix_par ^= 1u << st;
+        }
+        return true;
+      };
+      if (two) {
+        for (int x = 0; ok && x < 2; ++x) {
+          const int nx = x ? n : n_a;
+          if (nx > 0) ok = issue_s(x, qc + x, kc);
+          else ok = wait_all(&t.q_full[(qc + x) & 1], ((qc + x) >> 1) & 1, 0x54u);  // loaded all the same
+          if (ok && nx <= 1) tc_commit_w(&t.q_empty[(qc + x) & 1]);
+        }
+        if (ok) tc_commit_w(&t.k_empty[kc % STAGES]);
+        for (int i = 0; ok && i < n; ++i) {
+          for (int x = 0; ok && x < 2; ++x) {
+            const int nx = x ? n : n_a;
+            if (i >= nx) continue;
+            ok = before_pv(i) && issue_pv(x, kc + i, i == 0);
+            if (ok && i + 1 < nx) {
+              ok = issue_s(x, qc + x, kc + i + 1);
+              if (ok && i + 2 == nx) tc_commit_w(&t.q_empty[(qc + x) & 1]);
+            }
+          }
+          if (!ok) break;
+          tc_commit_w(&t.v_empty[(kc + i) % STAGES]);
+          if (i + 1 < n) tc_commit_w(&t.k_empty[(kc + i + 1) % STAGES]);
+        }
+        qc += 2;
+      } else {
+        for (int i = -2; ok && i < n; ++i) {
+          if (i >= 0) {
+            ok = before_pv(i) && issue_pv(i & 1, kc + i, i < 2);
+            if (ok) tc_commit_w(&t.v_empty[(kc + i) % STAGES]);
+          }
+          if (ok && i + 2 < n) {
+            ok = issue_s(i & 1, qc, kc + i + 2);
+            if (ok) tc_commit_w(&t.k_empty[(kc + i + 2) % STAGES]);
+            if (ok && i + 3 == n) tc_commit_w(&t.q_empty[qc & 1]);
+          }
+        }
+        qc += 1;
+      }
+      kc += n;
+      ++units;
+    }
+    tc_commit_w(&t.drain);
+    mbar_drain(&t.drain, 0, p.status);
+    __syncwarp();
+  } else if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
+    if (warp == 2) {
+      // It takes part in every tile, so that its parity waits skip no phase.
+      int kc = 0;
+      bool ok = true;
+      while (ok && walk_next(wk, t, p)) {
+        const PlanPiece pc = wk.pc;
+        const int L = pc.t0 < pc.t1 ? t.seq[pc.b].L : 0, from = L & (BKV - 1);
+        for (int j = pc.t0; j < pc.t1; ++j, ++kc) {
+          const int st = kc % STAGES;
+          ok = __all_sync(0xffffffffu, mbar_wait(&t.v_full[st], (kc / STAGES) & 1, abort_flag, p.status, p.wait_ns,
+                                                 0x5Au));
+          if (!ok) break;
+          if (from && j == L / BKV) {
+            // a row's 128 bytes stay its own under the swizzle
+            for (int ch = 0; ch < CH; ++ch) {
+              uint4 *rows = reinterpret_cast<uint4 *>(sV + st * TILE + ch * CHUNK + from * 128);
+              for (int e = lane; e < (BKV - from) * 8; e += 32) rows[e] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&t.v_fix[st]);
+          }
+          if (lane == 0) mbar_arrive(&t.v_empty[st]);
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HIGH));
+    // ---------------- softmax: warps 4..7 x = 0, warps 8..11 x = 1
+    const int x = (warp - 4) >> 2;
+    const int quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const int rt = r / p.G, rh = r - rt * p.G;  // this row's token of the tile and head of the group
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t s_col = x * BKV;
+    const float c2 = p.scale_log2;
+    uint32_t used = 0, joins = 0;  // tiles processed, exchanges with the other warpgroup
+    bool ok = true;
+    while (ok && walk_next(wk, t, p)) {
+      // what outlives the key loop is read again from the Walk
+      int t0, t1, step, own_tiles, mask_from, lim;
+      bool live, two;
+      {
+        const PlanPiece &pc = wk.pc;
+        const PlanSeq s = t.seq[pc.b];
+        const int tok0 = pc.p * 2 * p.tq;
+        two = s.n - tok0 > p.tq;
+        const int shift = two ? x * p.tq : 0;  // this tile's first token in the window
+        live = rt < p.tq && tok0 + shift + rt < s.n;
+        lim = live ? plan_visible(s, tok0 + shift + rt + 1) : 0;
+        mask_from = plan_visible(s, tok0 + shift + 1);
+        t0 = pc.t0;
+        t1 = pc.t1;
+        const int n = max(t1 - t0, 0);
+        if (two) {
+          const int n_a = max(min((plan_visible(s, tok0 + p.tq) + BKV - 1) / BKV, t1) - t0, 0);
+          own_tiles = x ? n : n_a;
+          step = 1;
+        } else {
+          own_tiles = (n + 1 - x) >> 1;
+          step = 2;
+        }
+      }
+      const bool any_live = __any_sync(0xffffffffu, live);
+      float m_run = -INFINITY, l = 0.f;
+      int j0 = (t0 + (step == 2 ? x : 0)) * BKV;
+      for (int i = 0; i < own_tiles; ++i, j0 += step * BKV) {
+        const uint32_t u = used + i;
+        ok = __all_sync(0xffffffffu, mbar_wait(&t.s_full[x], u & 1, abort_flag, p.status, p.wait_ns, 0x5Bu));
+        if (!ok) break;
+        if (!any_live) {  // a warp of padding rows: P may be anything
+          tc_fence_before();
+          mbar_arrive(&t.p_ready[2 * x]);
+          mbar_arrive(&t.p_ready[2 * x + 1]);
+          continue;
+        }
+        tc_fence_after();
+        uint32_t xr[BKV];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tmem_ld32(lane_base + s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(xr + 32 * c));
+        tmem_ld_wait();
+        if (j0 + BKV > mask_from) {  // slots past the tile's first query, past the last slot among them
+          const int vis = lim - j0;
+#pragma unroll
+          for (int c = 0; c < BKV; ++c)
+            if (c >= vis) xr[c] = 0xff800000u;  // -inf
+        }
+        float m8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m8[e] = __uint_as_float(xr[e]);
+#pragma unroll
+        for (int c = 8; c < BKV; c += 2)
+          m8[(c >> 1) & 7] = max3_nan(m8[(c >> 1) & 7], __uint_as_float(xr[c]), __uint_as_float(xr[c + 1]));
+        const float mt = max3_nan(max3_nan(m8[0], m8[1], m8[2]), max3_nan(m8[3], m8[4], m8[5]),
+                                  max_nan(m8[6], m8[7])) * c2;
+        const float m_new = max_nan(m_run, mt);
+        const bool need = live && !(m_new <= m_run + RESCALE_THRESHOLD);
+        if (__any_sync(0xffffffffu, need)) {
+          const float factor = (m_run == -INFINITY) ? 0.f : ex2(m_run - m_new);
+          if (i > 0) {  // O_x holds the tiles so far: wait for the last of them
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(&t.o_done[x], (u - 1) & 1, abort_flag, p.status, p.wait_ns, 0x5Cu));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(lane_base + 256 + x * 128 + c * 32, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+              tmem_st32(lane_base + 256 + x * 128 + c * 32, o);
+            }
+            tmem_st_wait();
+          }
+          l *= factor;
+          m_run = m_new;
+        }
+        const float neg_m = (m_run == -INFINITY) ? 0.f : -m_run;
+        const uint64_t cc = f2pack(c2, c2), mm = f2pack(neg_m, neg_m);
+        uint64_t s4[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const uint64_t a2 =
+                f2fma(f2pack(__uint_as_float(xr[h * 64 + 2 * e]), __uint_as_float(xr[h * 64 + 2 * e + 1])), cc, mm);
+            float e0, e1;
+            if (!EXACT && e % POLY_EVERY == POLY_EVERY - 1) {
+              exp2_poly2(a2, e0, e1);
+            } else {
+              float a0, a1;
+              f2unpack(a2, a0, a1);
+              e0 = ex2(a0);
+              e1 = ex2(a1);
+            }
+            s4[e & 3] = f2add(s4[e & 3], f2pack(e0, e1));
+            pk[e] = pack_bf16x2(e0, e1);
+          }
+          tmem_st32(lane_base + s_col + h * 32, pk);  // P over S: columns [32 h, 32 h + 32)
+          if (h == 0) {
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&t.p_ready[2 * x]);
+          }
+        }
+        {
+          float q0, q1, q2, q3;
+          f2unpack(f2add(s4[0], s4[1]), q0, q1);
+          f2unpack(f2add(s4[2], s4[3]), q2, q3);
+          l += (q0 + q1) + (q2 + q3);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&t.p_ready[2 * x + 1]);
+      }
+      if (!ok) break;
+      used += own_tiles;
+
+      // ---------------- end of the piece: O_x, or both O of a unit with one Q tile, leave TMEM
+      const bool any_tile = t1 > t0;
+      if (any_tile) {
+        // its own last PV; the other warpgroup's is known through the exchange
+        // below.  (A parity wait may skip no phase: S of a tile is issued
+        // after the PV before it on the same x, so that one has completed.)
+        if (own_tiles > 0)
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&t.o_done[x], (used - 1) & 1, abort_flag, p.status, p.wait_ns, 0x5Du));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      float f0 = x == 0 ? 1.f : 0.f, f1 = x == 0 ? 0.f : 1.f;  // O = f0 O_0 + f1 O_1
+      if (!two && any_tile) {
+        t.xchg[joins & 1][x][r] = make_float2(m_run, l);
+        tc_fence_before();
+        mbar_arrive(&t.x_full);
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&t.x_full, joins & 1, abort_flag, p.status, p.wait_ns, 0x5Eu));
+        if (!ok) break;
+        tc_fence_after();
+        const float2 a = t.xchg[joins & 1][0][r], b = t.xchg[joins & 1][1][r];
+        ++joins;
+        m_run = max_nan(a.x, b.x);
+        const float top = m_run == -INFINITY ? 0.f : m_run;
+        f0 = ex2(a.x - top);
+        f1 = ex2(b.x - top);
+        l = a.y * f0 + b.y * f1;
+      }
+      const PlanPiece &pc = wk.pc;
+      const int g = wk.group * p.group_heads + pc.g;
+      const int row = (two ? x * p.tq : 0) + rt;                   // token inside the window
+      const int tok = t.first[pc.b] + pc.p * 2 * p.tq + row;       // packed row
+      const int head = g * p.G + rh;
+      const int64_t part = (static_cast<int64_t>(wk.group) * gridDim.x + blockIdx.x) * 2 + pc.slot;
+      const bool whole = pc.whole != 0;
+      // columns this warpgroup writes: all of its own O, or its half of the joined one
+      const int c0 = two ? 0 : x * (D / 64), c1 = two ? D / 32 : (x + 1) * (D / 64);
+      const bool first_wg = two || x == 0;
+      if (live && first_wg) {
+        if (whole) {
+          if (p.lse) p.lse[static_cast<int64_t>(tok) * p.Hq + head] = (m_run + log2f(l)) * LN2;
+        } else if (any_tile) {
+          p.part_ml[part * SLOT_ROWS + row * p.G + rh] = make_float2(m_run, l);
+        }
+      }
+      const float inv = whole ? (lim == 0 ? 0.f : 1.f / l) : 1.f;
+      f0 *= inv;
+      f1 *= inv;
+      const bool use0 = two ? x == 0 && own_tiles > 0 : any_tile;
+      const bool use1 = two ? x == 1 && own_tiles > 0 : t1 - t0 > 1;
+      if (any_live && (whole || any_tile)) {
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+          if (use0) {
+            uint32_t o[32];
+            tmem_ld32(lane_base + 256 + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f0;
+          }
+          if (use1) {
+            uint32_t o[32];
+            tmem_ld32(lane_base + 384 + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
+          }
+          if (!live) continue;
+          if (whole) {
+            if (lim == 0) {  // no slot is visible
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = 0.f;
+            }
+            uint4 *dst = reinterpret_cast<uint4 *>(p.o + tok * p.o_stride + head * D + c * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              dst[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                                  pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+          } else {
+            float4 *dst = reinterpret_cast<float4 *>(p.part_o + (part * SLOT_ROWS + row * p.G + rh) * D + c * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          }
+        }
+      }
+      if (any_tile) {
+        tc_fence_before();
+        mbar_arrive(&t.o_free);
+      }
+    }
+  }
+  // what this CTA's ranges leave for the combine kernel
+  if (threadIdx.x < p.groups) {
+    const int heads = heads_of(p, threadIdx.x), rg = blockIdx.x;
+    PlanCut cut{};
+    cut.total = t.before[p.c.B] * heads;
+    const int nr = plan_ranges(cut.total, gridDim.x);
+    if (rg < nr && cut.total > 0) {
+      PlanCursor cur;
+      plan_open(cur, t.seq, t.before, p.c.B, 2 * p.tq, heads, plan_cut(cut.total, nr, rg), 1);
+      cut = PlanCut{cut.total, nr, cur.b, cur.p, cur.g, cur.off, cur.c};
+    }
+    p.cuts[threadIdx.x * gridDim.x + rg] = cut;
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the pieces of the unit whose first cut is in front of range
+// blockIdx.x + 1 of group blockIdx.y: O = sum_i 2^(m_i - m) O_i / sum_i
+// 2^(m_i - m) l_i, the pieces in order, one warp per row.
+constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_SPLIT = 8;  // CTAs per unit
+
 template <int D>
-__global__ void __launch_bounds__(128) paged_attn_rows_kernel(PagedView c, PagedAttnArgs a) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(JOIN_THREADS) paged_combine_kernel(const __grid_constant__ Params p, int ctas) {
+  const int range = blockIdx.x + 1, group = blockIdx.y;
+  const PlanCut cut = p.cuts[group * ctas + range];
+  if (!plan_first_cut(cut, range)) return;
+  int first, n;
+  packed_span(p.cu, p.T, cut.b, nullptr, first, n);
+  const PlanSeq s{n, paged_len(p.c, cut.b, nullptr)};
+  const int w = 2 * p.tq, tok0 = cut.p * w, g = group * p.group_heads + cut.g;
+  const int rows = min(w, n - tok0) * p.G;
+  const int tiles = (plan_visible(s, tok0 + w) + BKV - 1) / BKV;
   const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int t = static_cast<int>(unit / a.Hq), h = static_cast<int>(unit % a.Hq), g = h / (a.Hq / c.Hkv);
-  Row r;
-  if (blockIdx.x == 0) check_sequences(c, a.cu, static_cast<int>(a.T), a.status);
-  if (t >= a.T || !row_of(c, a.cu, static_cast<int>(a.T), t, nullptr, r)) return;
-  const int end = max(r.L - r.n + r.i + 1, 0);
-  float q[E], acc[E], m = -INFINITY, l = 0.f;
-  const __nv_bfloat16 *qr = static_cast<const __nv_bfloat16 *>(a.q) + t * a.q_stride + h * D + lane * E;
+  constexpr int E = D / 32;
+  for (int row = blockIdx.z * (JOIN_THREADS / 32) + (threadIdx.x >> 5); row < rows;
+       row += JOIN_SPLIT * (JOIN_THREADS / 32)) {
+    float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(qr[e]) * a.scale;
-    acc[e] = 0.f;
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int i = 0, end = 0; end != cut.c; ++i) {
+      int rg, slot, off, t0, t1;
+      plan_piece_of(cut, range, i, rg, slot, off, end);
+      plan_tiles(off, end, cut.c, tiles, t0, t1);
+      if (t0 >= t1) continue;
+      const int64_t part = ((static_cast<int64_t>(group) * ctas + rg) * 2 + slot) * SLOT_ROWS + row;
+      const float2 ml = p.part_ml[part];
+      if (ml.x == -INFINITY) continue;  // this row sees nothing of the piece
+      const float mn = max_nan(m, ml.x), fa = m == -INFINITY ? 0.f : ex2(m - mn), fb = ex2(ml.x - mn);
+      const float *o = p.part_o + part * D + lane * E;
+      l = l * fa + ml.y * fb;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(o[e], fb, acc[e] * fa);
+      m = mn;
+    }
+    const int tok = first + tok0 + row / p.G, head = g * p.G + row % p.G;
+    const bool none = plan_visible(s, tok0 + row / p.G + 1) == 0;
+    const float inv = none ? 0.f : 1.f / l;
+    __nv_bfloat16 *o = p.o + tok * p.o_stride + head * D + lane * E;
+    uint32_t packed[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) packed[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (E == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(packed[0], packed[E / 2 - 1]);
+    else *reinterpret_cast<uint32_t *>(o) = packed[0];
+    if (lane == 0 && p.lse)
+      p.lse[static_cast<int64_t>(tok) * p.Hq + head] = none ? -INFINITY : (m + log2f(l)) * LN2;
   }
-  int page = -1;
-  for (int j = 0; j < end; ++j) {
-    if ((j & ((1 << c.page_shift) - 1)) == 0)
-      page = paged_page(c.table, c.table_stride, c.num_pages, r.b, j >> c.page_shift, lane == 0 ? a.status : nullptr);
-    if (page < 0) continue;
-    const int64_t at = paged_offset(c, page, j, g) + lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], __bfloat162float(c.k[at + e]), s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float mn = fmaxf(m, s);
-    const float top = mn == -INFINITY ? 0.f : mn;  // no score above -inf yet (a NaN keeps its p NaN)
-    const float f = m == -INFINITY ? 0.f : expf(m - mn), p = expf(s - top);
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(p, __bfloat162float(c.v[at + e]), acc[e] * f);
-    m = mn;
-  }
-  __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + t * a.o_stride + h * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = __float2bfloat16(l == 0.f ? 0.f : acc[e] / l);
-  if (lane == 0 && a.lse) a.lse[static_cast<int64_t>(t) * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 // One thread per (sequence, weight row, slot): the weights of every new row
@@ -94,15 +780,97 @@ __global__ void __launch_bounds__(128) paged_weights_kernel(PagedView c, PagedAt
   a.weights[(static_cast<int64_t>(b) * a.Hs + hs) * a.w_stride + j] += sum;
 }
 
+
+struct Scratch {
+  float *part_o;
+  float2 *part_ml;
+  PlanCut *cuts;
+  size_t bytes;
+};
+
+Scratch carve(void *base, int d, int groups, int ctas) {
+  char *at = static_cast<char *>(base);
+  const size_t slots = static_cast<size_t>(groups) * ctas * 2 * SLOT_ROWS;
+  Scratch s;
+  s.part_o = reinterpret_cast<float *>(at);
+  size_t off = Carver::round(slots * d * sizeof(float));
+  s.part_ml = reinterpret_cast<float2 *>(at + off);
+  off += Carver::round(slots * sizeof(float2));
+  s.cuts = reinterpret_cast<PlanCut *>(at + off);
+  off += Carver::round(sizeof(PlanCut) * groups * ctas);
+  s.bytes = off;
+  return s;
+}
+
+constexpr int GROUPS = 1;
+
+template <int D, bool EXACT>
+spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, int ctas,
+                   cudaStream_t s) {
+  SPTS_CUDA_TRY(cudaFuncSetAttribute(paged_attn_kernel<D, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(smem_bytes<D>())));
+  paged_attn_kernel<D, EXACT><<<ctas, THREADS, smem_bytes<D>(), s>>>(tq, tk, tv, p);
+  note_launch();
+  SPTS_CUDA_TRY(cudaGetLastError());
+  if (ctas > 1) {
+    paged_combine_kernel<D><<<dim3(ctas - 1, p.groups, JOIN_SPLIT), JOIN_THREADS, 0, s>>>(p, ctas);
+    note_launch();
+    SPTS_CUDA_TRY(cudaGetLastError());
+  }
+  return SPTS_OK;
+}
+
 }  // namespace
+
+size_t paged_attn_scratch_bytes(int d) { return carve(nullptr, d, GROUPS, num_sms()).bytes; }
 
 spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, cudaStream_t s) {
   if (a.T == 0) return SPTS_OK;
-  const unsigned blocks = static_cast<unsigned>((a.T * a.Hq + 3) / 4);
-  if (c.d == 64) paged_attn_rows_kernel<64><<<blocks, 128, 0, s>>>(c, a);
-  else paged_attn_rows_kernel<128><<<blocks, 128, 0, s>>>(c, a);
-  note_launch();
-  SPTS_CUDA_TRY(cudaGetLastError());
+  const int D = c.d, G = a.Hq / c.Hkv, tq = 128 / G, ctas = num_sms();
+  CUtensorMap tq_map, tk_map, tv_map;
+  {
+    uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.T)};
+    uint64_t strides[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a.q_stride) * 2};
+    uint32_t box[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(tq)};
+    SPTS_TRY(make_tmap(&tq_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B));
+  }
+  {
+    const int page = 1 << c.page_shift;
+    uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(c.Hkv), static_cast<uint64_t>(page),
+                        static_cast<uint64_t>(c.num_pages)};
+    uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(c.Hkv) * D * 2,
+                           static_cast<uint64_t>(c.page_stride) * 2};
+    uint32_t box[4] = {64, 1, static_cast<uint32_t>(page < BKV ? page : BKV), 1};
+    SPTS_TRY(make_tmap(&tk_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.k, dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B));
+    SPTS_TRY(make_tmap(&tv_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.v, dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B));
+  }
+  const Scratch sc = carve(a.scratch, D, GROUPS, ctas);
+  Params p{};
+  p.c = c;
+  p.cu = a.cu;
+  p.T = static_cast<int>(a.T);
+  p.Hq = a.Hq;
+  p.G = G;
+  p.tq = tq;
+  p.groups = GROUPS;
+  p.group_heads = (c.Hkv + GROUPS - 1) / GROUPS;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.o = static_cast<__nv_bfloat16 *>(a.o);
+  p.o_stride = a.o_stride;
+  p.lse = a.lse;
+  p.part_o = sc.part_o;
+  p.part_ml = sc.part_ml;
+  p.cuts = sc.cuts;
+  p.status = a.status;
+  p.wait_ns = wait_limit_ns();
+  const bool exact = a.lse != nullptr;
+  if (D == 64)
+    SPTS_TRY((exact ? launch<64, true> : launch<64, false>)(tq_map, tk_map, tv_map, p, ctas, s));
+  else
+    SPTS_TRY((exact ? launch<128, true> : launch<128, false>)(tq_map, tk_map, tv_map, p, ctas, s));
   if (a.weights == nullptr) return SPTS_OK;
   const int cap = c.max_pages << c.page_shift;
   const dim3 grid(static_cast<unsigned>((cap + 127) / 128), static_cast<unsigned>(c.B) * a.Hs);

@@ -52,6 +52,26 @@ struct PlanUnit {
   int off, c;
 };
 
+// First slot that no token of [window start, window start + tokens) sees, for
+// tokens counted inside the sequence's new ones.
+SPTS_HD int plan_visible(const PlanSeq &s, int last_token_end) {
+  return plan_max(s.L - s.n + plan_min(last_token_end, s.n), 0);
+}
+
+// Key tiles of the piece [off, end) of a unit with cost c and `tiles` tiles:
+// every tile belongs to exactly one piece.
+SPTS_HD void plan_tiles(int off, int end, int c, int tiles, int &t0, int &t1) {
+  t0 = plan_min(tiles, (off + PLAN_TILE - 1) / PLAN_TILE);
+  t1 = end == c ? tiles : plan_min(tiles, (end + PLAN_TILE - 1) / PLAN_TILE);
+}
+
+// Ranges a group of total cost `total` is cut into: none shorter than a tile.
+SPTS_HD int plan_ranges(int64_t total, int ctas) {
+  const int64_t r = total / PLAN_TILE;
+  return r < 1 ? 1 : (r < ctas ? static_cast<int>(r) : ctas);
+}
+
+
 // y: position inside the sequence's units of one head group of `heads` heads.
 SPTS_HD PlanUnit plan_locate(const PlanSeq &s, int w, int heads, int64_t y) {
   const int base = plan_base(s);
@@ -70,23 +90,96 @@ SPTS_HD PlanUnit plan_locate(const PlanSeq &s, int w, int heads, int64_t y) {
   return u;
 }
 
-// First slot that no token of [window start, window start + tokens) sees, for
-// tokens counted inside the sequence's new ones.
-SPTS_HD int plan_visible(const PlanSeq &s, int last_token_end) {
-  return plan_max(s.L - s.n + plan_min(last_token_end, s.n), 0);
+// A walk over the pieces of one range.
+struct PlanCursor {
+  int b, p, g;   // the unit the walk stands in
+  int off, c;    // how far into it, and its cost
+  int64_t left;  // what is left of the range
+};
+
+struct PlanPiece {
+  int b, p, g;
+  int off, c;         // where in its unit it begins (at the start of a walk this may be > 0), the unit's cost
+  int t0, t1, tiles;  // its key tiles, and how many the unit has
+  int whole;          // the piece is the unit
+  int slot;           // otherwise: where its partial result goes (0: it begins inside the unit, 1: at its start)
+};
+
+// Stands a walk at position x of a group of `heads` heads; before[b] is the
+// cost of the sequences before b for one head (before[B]: of all).
+SPTS_HD void plan_open(PlanCursor &cur, const PlanSeq *seq, const int64_t *before, int B, int w, int heads, int64_t x,
+                       int64_t length) {
+  int lo = 0, hi = B - 1;  // the last sequence that begins at or before x and has any cost
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (before[mid] * heads <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  cur.left = length;
+  cur.b = lo;
+  if (length <= 0) return;
+  const PlanUnit u = plan_locate(seq[lo], w, heads, x - before[lo] * heads);
+  cur.p = u.p;
+  cur.g = u.g;
+  cur.off = u.off;
+  cur.c = u.c;
 }
 
-// Key tiles of the piece [off, end) of a unit with cost c and `tiles` tiles:
-// every tile belongs to exactly one piece.
-SPTS_HD void plan_tiles(int off, int end, int c, int tiles, int &t0, int &t1) {
-  t0 = plan_min(tiles, (off + PLAN_TILE - 1) / PLAN_TILE);
-  t1 = end == c ? tiles : plan_min(tiles, (end + PLAN_TILE - 1) / PLAN_TILE);
+// The next piece, or 0 at the end of the range.
+SPTS_HD int plan_next(PlanCursor &cur, const PlanSeq *seq, int B, int w, int heads, PlanPiece &pc) {
+  if (cur.left <= 0 || cur.b >= B) return 0;
+  const PlanSeq s = seq[cur.b];
+  const int take = static_cast<int>(cur.left < cur.c - cur.off ? cur.left : cur.c - cur.off);
+  pc.b = cur.b;
+  pc.p = cur.p;
+  pc.g = cur.g;
+  pc.off = cur.off;
+  pc.c = cur.c;
+  pc.tiles = (plan_visible(s, (cur.p + 1) * w) + PLAN_TILE - 1) / PLAN_TILE;
+  plan_tiles(cur.off, cur.off + take, cur.c, pc.tiles, pc.t0, pc.t1);
+  pc.whole = take == cur.c;
+  pc.slot = cur.off > 0 ? 0 : 1;
+  cur.left -= take;
+  if (cur.off + take == cur.c) {
+    cur.off = 0;
+    if (++cur.g == heads) {
+      cur.g = 0;
+      if (++cur.p == plan_windows(s.n, w)) {
+        cur.p = 0;
+        do ++cur.b;
+        while (cur.b < B && seq[cur.b].n <= 0);
+      }
+    }
+    if (cur.b < B) cur.c = plan_base(seq[cur.b]) + (cur.p + 1) * w;
+  } else {
+    cur.off += take;
+  }
+  return 1;
 }
 
-// Ranges a group of total cost `total` is cut into: none shorter than a tile.
-SPTS_HD int plan_ranges(int64_t total, int ctas) {
-  const int64_t r = total / PLAN_TILE;
-  return r < 1 ? 1 : (r < ctas ? static_cast<int>(r) : ctas);
+// What the range r leaves for the combine kernel about its first position.
+struct PlanCut {
+  int64_t total;  // cost of the group
+  int nr;         // its ranges (0: this range is not one of them)
+  int b, p, g;    // the unit at the cut
+  int off, c;     // how far inside it the cut is (0: between two units), and the unit's cost
+};
+
+// Whether the cut in front of range r is the first one inside its unit.
+SPTS_HD int plan_first_cut(const PlanCut &cut, int r) {
+  return r > 0 && r < cut.nr && cut.off > 0 &&
+         plan_cut(cut.total, cut.nr, r) - cut.off >= plan_cut(cut.total, cut.nr, r - 1);
+}
+
+// Piece i of the unit whose first cut is in front of range r: the range that
+// computed it, its slot there, and its [off, end) in the unit.
+SPTS_HD void plan_piece_of(const PlanCut &cut, int r, int i, int &range, int &slot, int &off, int &end) {
+  const int64_t start = plan_cut(cut.total, cut.nr, r) - cut.off;
+  range = r - 1 + i;
+  slot = i == 0 ? 1 : 0;
+  off = i == 0 ? 0 : static_cast<int>(plan_cut(cut.total, cut.nr, range) - start);
+  const int64_t e = plan_cut(cut.total, cut.nr, range + 1) - start;
+  end = e < cut.c ? static_cast<int>(e) : cut.c;
 }
 
 }  // namespace spts
