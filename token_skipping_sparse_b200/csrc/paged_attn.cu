@@ -124,15 +124,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
-                                            int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
-      "%6}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
-}
-
 __device__ __forceinline__ int heads_of(const Params &p, int group) {
   return min(p.group_heads, p.c.Hkv - group * p.group_heads);
 }
@@ -756,31 +747,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_combine_kernel(const __gri
   }
 }
 
-// One thread per (sequence, weight row, slot): the weights of every new row
-// and head over again, from the rows' lse.
-template <int D>
-__global__ void __launch_bounds__(128) paged_weights_kernel(PagedView c, PagedAttnArgs a) {
-  const int b = blockIdx.y / a.Hs, hs = blockIdx.y % a.Hs, j = blockIdx.x * 128 + threadIdx.x;
-  int first, n;
-  packed_span(a.cu, static_cast<int>(a.T), b, nullptr, first, n);
-  const int L = paged_len(c, b, nullptr);
-  if (j >= L || n == 0) return;
-  const int page = paged_page(c.table, c.table_stride, c.num_pages, b, j >> c.page_shift, a.status);
-  if (page < 0) return;
-  const int heads = a.Hq / a.Hs, G = a.Hq / c.Hkv;
-  float sum = 0.f;
-  for (int i = max(0, j - (L - n)); i < n; ++i)
-    for (int h = hs * heads; h < (hs + 1) * heads; ++h) {
-      const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + (first + i) * a.q_stride + h * D;
-      const __nv_bfloat16 *k = c.k + paged_offset(c, page, j, h / G);
-      float s = 0.f;
-      for (int e = 0; e < D; ++e) s = fmaf(__bfloat162float(q[e]) * a.scale, __bfloat162float(k[e]), s);
-      sum += expf(s - a.lse[static_cast<int64_t>(first + i) * a.Hq + h]);
-    }
-  a.weights[(static_cast<int64_t>(b) * a.Hs + hs) * a.w_stride + j] += sum;
-}
-
-
 struct Scratch {
   float *part_o;
   float2 *part_ml;
@@ -822,31 +788,27 @@ spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
 
 }  // namespace
 
+spts_status paged_maps(const PagedView &c, const PagedAttnArgs &a, CUtensorMap *q, CUtensorMap *k, CUtensorMap *v) {
+  const uint64_t D = c.d, G = a.Hq / c.Hkv, page = uint64_t(1) << c.page_shift;
+  const uint64_t q_dims[3] = {D, static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.T)};
+  const uint64_t q_strides[2] = {D * 2, static_cast<uint64_t>(a.q_stride) * 2};
+  const uint32_t q_box[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(128 / G)};
+  SPTS_TRY(make_tmap(q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, q_dims, q_strides, q_box,
+                     CU_TENSOR_MAP_SWIZZLE_128B));
+  const uint64_t dims[4] = {D, static_cast<uint64_t>(c.Hkv), page, static_cast<uint64_t>(c.num_pages)};
+  const uint64_t strides[3] = {D * 2, static_cast<uint64_t>(c.Hkv) * D * 2, static_cast<uint64_t>(c.page_stride) * 2};
+  const uint32_t box[4] = {64, 1, static_cast<uint32_t>(page < PLAN_TILE ? page : PLAN_TILE), 1};
+  SPTS_TRY(make_tmap(k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B));
+  return make_tmap(v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 size_t paged_attn_scratch_bytes(int d) { return carve(nullptr, d, GROUPS, num_sms()).bytes; }
 
 spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, cudaStream_t s) {
   if (a.T == 0) return SPTS_OK;
   const int D = c.d, G = a.Hq / c.Hkv, tq = 128 / G, ctas = num_sms();
   CUtensorMap tq_map, tk_map, tv_map;
-  {
-    uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.T)};
-    uint64_t strides[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a.q_stride) * 2};
-    uint32_t box[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(tq)};
-    SPTS_TRY(make_tmap(&tq_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dims, strides, box,
-                       CU_TENSOR_MAP_SWIZZLE_128B));
-  }
-  {
-    const int page = 1 << c.page_shift;
-    uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(c.Hkv), static_cast<uint64_t>(page),
-                        static_cast<uint64_t>(c.num_pages)};
-    uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(c.Hkv) * D * 2,
-                           static_cast<uint64_t>(c.page_stride) * 2};
-    uint32_t box[4] = {64, 1, static_cast<uint32_t>(page < BKV ? page : BKV), 1};
-    SPTS_TRY(make_tmap(&tk_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.k, dims, strides, box,
-                       CU_TENSOR_MAP_SWIZZLE_128B));
-    SPTS_TRY(make_tmap(&tv_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.v, dims, strides, box,
-                       CU_TENSOR_MAP_SWIZZLE_128B));
-  }
+  SPTS_TRY(paged_maps(c, a, &tq_map, &tk_map, &tv_map));
   const Scratch sc = carve(a.scratch, D, GROUPS, ctas);
   Params p{};
   p.c = c;
@@ -871,14 +833,7 @@ spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, c
     SPTS_TRY((exact ? launch<64, true> : launch<64, false>)(tq_map, tk_map, tv_map, p, ctas, s));
   else
     SPTS_TRY((exact ? launch<128, true> : launch<128, false>)(tq_map, tk_map, tv_map, p, ctas, s));
-  if (a.weights == nullptr) return SPTS_OK;
-  const int cap = c.max_pages << c.page_shift;
-  const dim3 grid(static_cast<unsigned>((cap + 127) / 128), static_cast<unsigned>(c.B) * a.Hs);
-  if (c.d == 64) paged_weights_kernel<64><<<grid, 128, 0, s>>>(c, a);
-  else paged_weights_kernel<128><<<grid, 128, 0, s>>>(c, a);
-  note_launch();
-  SPTS_CUDA_TRY(cudaGetLastError());
-  return SPTS_OK;
+  return a.weights ? launch_paged_weights(c, a, tq_map, tk_map, s) : SPTS_OK;
 }
 
 }  // namespace spts
