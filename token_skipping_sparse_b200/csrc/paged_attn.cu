@@ -128,6 +128,11 @@ __device__ __forceinline__ int heads_of(const Params &p, int group) {
   return min(p.group_heads, p.c.Hkv - group * p.group_heads);
 }
 
+// A value that all lanes hold, so that the compiler knows it too: loop counts
+// and ring places then live in uniform registers, where the MMA descriptors
+// have to be (2048 rows over 32K slots: TODO).
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // The warp's next piece of this CTA's ranges, group after group, into its own
 // Walk (lane 0 steps, all lanes read).
 __device__ __forceinline__ bool walk_next(Walk &wk, const Tail &t, const Params &p) {
@@ -150,7 +155,7 @@ __device__ __forceinline__ bool walk_next(Walk &wk, const Tail &t, const Params 
     }
   }
   __syncwarp();
-  return wk.more != 0;
+  return uniform(wk.more) != 0;
 }
 
 // Lengths and offsets of all sequences, and their costs added up.
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   read_sequences(t, p);  // ends with __syncthreads
   tc_fence_after();
-  const uint32_t tmem = t.tmem;
+  const uint32_t tmem = uniform(t.tmem);
   Walk &wk = t.walk[warp];
 
   if (warp == 0) {
@@ -351,14 +356,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       return true;
     };
     while (ok && walk_next(wk, t, p)) {
-      const PlanPiece pc = wk.pc;
-      if (pc.t0 >= pc.t1) continue;
-      const PlanSeq s = t.seq[pc.b];
-      const int tok0 = pc.p * 2 * p.tq, n = pc.t1 - pc.t0;
+      const PlanPiece &pc = wk.pc;
+      const int t0 = uniform(pc.t0), n = uniform(pc.t1) - t0;
+      if (n <= 0) continue;
+      const PlanSeq s{uniform(t.seq[pc.b].n), uniform(t.seq[pc.b].L)};
+      const int tok0 = uniform(pc.p) * 2 * p.tq;
       const bool two = s.n - tok0 > p.tq;
       // tiles of x = 0 when it has a Q tile of its own
-      const int n_a = two ? max(min((plan_visible(s, tok0 + p.tq) + BKV - 1) / BKV, pc.t1) - pc.t0, 0) : 0;
-      const int fix = (s.L & (BKV - 1)) ? s.L / BKV - pc.t0 : -1;  // the tile that warp 2 mends
+      const int n_a = two ? max(min((plan_visible(s, tok0 + p.tq) + BKV - 1) / BKV - t0, n), 0) : 0;
+      const int fix = (s.L & (BKV - 1)) ? s.L / BKV - t0 : -1;  // the tile that warp 2 mends
       bool fixed = fix < 0 || fix >= n;
       bool free_ = false;
       auto before_pv = [&](int i) -> bool {  // O free of the last unit, V of tile i mended
