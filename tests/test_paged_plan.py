@@ -23,7 +23,7 @@ extern "C" int walk(int B, const int *n, const int *L, int w, int heads, int cta
   std::vector<int64_t> before(B + 1, 0);
   for (int b = 0; b < B; ++b) {
     seq[b] = PlanSeq{n[b], L[b]};
-    before[b + 1] = before[b] + plan_cost(plan_base(seq[b]), plan_windows(n[b], w), w);
+    before[b + 1] = before[b] + plan_cost(plan_base(seq[b], w), plan_windows(n[b], w), w);
   }
   const int64_t total = before[B] * heads;
   const int nr = plan_ranges(total, ctas);

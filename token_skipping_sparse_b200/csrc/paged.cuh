@@ -8,8 +8,9 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <utility>
 
-#include "spts.h"
+#include "host.hpp"
 #include "status.cuh"
 
 namespace spts {
@@ -71,6 +72,24 @@ __device__ __forceinline__ int paged_page(const int32_t *table, int64_t stride, 
 // Element offset of slot t's row of KV head g inside page `page`.
 __device__ __forceinline__ int64_t paged_offset(const PagedView &c, int page, int t, int g) {
   return page * c.page_stride + (static_cast<int64_t>(t & ((1 << c.page_shift) - 1)) * c.Hkv + g) * c.d;
+}
+
+// Launches a kernel that may start while the one before it on the stream still
+// runs, and waits for it itself (griddepcontrol.wait).
+template <typename... Want, typename... Args>
+spts_status launch_behind(void (*kernel)(Want...), dim3 grid, int threads, cudaStream_t s, Args &&...args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  SPTS_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...));
+  note_launch();
+  return SPTS_OK;
 }
 
 spts_status launch_cache_append(const PagedView &c, const void *k_new, int64_t k_stride, const void *v_new,

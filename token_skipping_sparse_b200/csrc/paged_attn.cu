@@ -23,7 +23,8 @@
 //               from TMEM; the loop runs across units without a drain;
 //   warp 2      zeroes the V rows behind the sequence's last slot in its last
 //               tile: they may hold anything, and 0 x NaN is NaN;
-//   warp 3      idle (completes the warpgroup for the register split);
+//   warp 3      walks the plan and hands the pieces to the other warps through
+//               a ring of ITEMS places, ahead of them;
 //   warps 4..7, 8..11  softmax, one thread per row, one warpgroup per S_x.
 // A unit with two tiles gives them to x = 0 and 1, and every K/V tile feeds
 // both.  A unit with one (n <= tq: decoding) gives the even key tiles to x = 0
@@ -67,10 +68,20 @@ struct Geometry {
   static constexpr int OFF_TAIL = OFF_V + STAGES * TILE;
 };
 
-struct Walk {
-  PlanCursor cur;
-  PlanPiece pc;
-  int group, more;
+constexpr int ITEMS = 4;
+
+// A piece of a unit, as the warps need it.
+struct Item {
+  int more;           // 0 behind the last piece
+  int b, n, L;        // the sequence, its new and cached tokens
+  int first;          // packed row of its first new token
+  int tok0;           // first token of the window
+  int g;              // KV head
+  int two;            // whether the window fills a second Q tile
+  int t0, t1;         // key tiles
+  int a_end;          // with two Q tiles: end of those that the first one sees
+  int whole;          // the piece is the unit
+  int part;           // otherwise: place of its partial result
 };
 
 struct Tail {  // shared memory behind the tiles
@@ -81,7 +92,8 @@ struct Tail {  // shared memory behind the tiles
   uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t v_fix[4];  // per stage, so that warp 2 cannot be two phases ahead of the MMA warp
   uint64_t s_full[2], p_ready[4], o_done[2], o_free, x_full, drain;
-  Walk walk[12];
+  uint64_t item_full[ITEMS], item_empty[ITEMS];
+  Item item[ITEMS];
   uint32_t tmem;
   int abort_flag;
 };
@@ -124,6 +136,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// 32 bytes at once: a row's thread writes whole sectors.
+__device__ __forceinline__ void store_8(float *to, const float *v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
 __device__ __forceinline__ int heads_of(const Params &p, int group) {
   return min(p.group_heads, p.c.Hkv - group * p.group_heads);
 }
@@ -133,29 +152,53 @@ __device__ __forceinline__ int heads_of(const Params &p, int group) {
 // have to be (2048 rows over 32K slots: TODO).
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// The warp's next piece of this CTA's ranges, group after group, into its own
-// Walk (lane 0 steps, all lanes read).
-__device__ __forceinline__ bool walk_next(Walk &wk, const Tail &t, const Params &p) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    wk.more = 1;
-    while (wk.group < 0 || !plan_next(wk.cur, t.seq, p.c.B, 2 * p.tq, heads_of(p, wk.group), wk.pc)) {
-      if (++wk.group == p.groups) {
-        wk.more = 0;
-        break;
-      }
-      const int heads = heads_of(p, wk.group), r = blockIdx.x;
-      const int64_t total = t.before[p.c.B] * heads;
-      const int nr = plan_ranges(total, gridDim.x);
-      wk.cur.left = 0;
-      if (r < nr) {
-        const int64_t x = plan_cut(total, nr, r);
-        plan_open(wk.cur, t.seq, t.before, p.c.B, 2 * p.tq, heads, x, plan_cut(total, nr, r + 1) - x);
-      }
+// Warp 3, one lane: the pieces of this CTA's ranges, group after group.
+__device__ __forceinline__ void walk(Tail &t, const Params &p) {
+  volatile int *abort_flag = &t.abort_flag;
+  const int w = 2 * p.tq, r = blockIdx.x;
+  int count = 0;
+  bool ok = true;
+  auto place = [&]() -> Item * {  // the next free place of the ring
+    const int i = count % ITEMS;
+    ok = mbar_wait(&t.item_empty[i], ((count / ITEMS) & 1) ^ 1, abort_flag, p.status, p.wait_ns, 0x50u);
+    return &t.item[i];
+  };
+  for (int group = 0; ok && group < p.groups; ++group) {
+    const int heads = heads_of(p, group);
+    const int64_t total = t.before[p.c.B] * heads;
+    const int nr = plan_ranges(total, gridDim.x);
+    if (r >= nr) continue;
+    const int64_t x = plan_cut(total, nr, r);
+    PlanCursor cur;
+    plan_open(cur, t.seq, t.before, p.c.B, w, heads, x, plan_cut(total, nr, r + 1) - x);
+    PlanPiece pc;
+    while (ok && plan_next(cur, t.seq, p.c.B, w, heads, pc)) {
+      const PlanSeq s = t.seq[pc.b];
+      if (pc.t0 >= pc.t1 && !pc.whole) continue;  // nothing to compute, nothing to write
+      Item *it = place();
+      if (!ok) break;
+      it->more = 1;
+      it->b = pc.b;
+      it->n = s.n;
+      it->L = s.L;
+      it->first = t.first[pc.b];
+      it->tok0 = pc.p * w;
+      it->g = group * p.group_heads + pc.g;
+      it->two = s.n - pc.p * w > p.tq;
+      it->t0 = pc.t0;
+      it->t1 = pc.t1;
+      it->a_end = (plan_visible(s, pc.p * w + p.tq) + BKV - 1) / BKV;
+      it->whole = pc.whole;
+      it->part = (group * static_cast<int>(gridDim.x) + r) * 2 + pc.slot;
+      mbar_arrive(&t.item_full[count % ITEMS]);
+      ++count;
     }
   }
-  __syncwarp();
-  return uniform(wk.more) != 0;
+  if (!ok) return;
+  Item *it = place();
+  if (!ok) return;
+  it->more = 0;
+  mbar_arrive(&t.item_full[count % ITEMS]);
 }
 
 // Lengths and offsets of all sequences, and their costs added up.
@@ -174,7 +217,7 @@ __device__ __forceinline__ void read_sequences(Tail &t, const Params &p) {
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
       const int b = b0 + lane;
       int64_t x = 0;
-      if (b < p.c.B) x = plan_cost(plan_base(t.seq[b]), plan_windows(t.seq[b].n, 2 * p.tq), 2 * p.tq);
+      if (b < p.c.B) x = plan_cost(plan_base(t.seq[b], 2 * p.tq), plan_windows(t.seq[b].n, 2 * p.tq), 2 * p.tq);
       int64_t incl = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -201,6 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int *abort_flag = &t.abort_flag;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) raise_status(p.status, SPTS_DEV_BADINDEX, 0x5Fu, smem_u32(smem));
     return;
@@ -223,11 +267,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     mbar_init(&t.o_free, 256);
     mbar_init(&t.x_full, 256);
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(&t.item_full[i], 1);
+      mbar_init(&t.item_empty[i], 11);  // a lane of every other warp
+    }
     mbar_init(&t.drain, 1);
     t.abort_flag = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x < 12) t.walk[threadIdx.x].group = -1;
   if (warp == 1) {
     tmem_alloc(&t.tmem, TMEM_COLS);
     tmem_relinquish();
@@ -236,7 +283,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   read_sequences(t, p);  // ends with __syncthreads
   tc_fence_after();
   const uint32_t tmem = uniform(t.tmem);
-  Walk &wk = t.walk[warp];
+  // The i-th item for this warp, or null behind the last one (or on the way
+  // out); give_back lets warp 3 reuse its place.
+  auto take = [&](int i) -> const Item * {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(&t.item_full[i % ITEMS], (i / ITEMS) & 1, abort_flag, p.status,
+                                                      p.wait_ns, 0x5Fu));
+    const Item *it = &t.item[i % ITEMS];
+    return ok && uniform(it->more) ? it : nullptr;
+  };
+  auto give_back = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&t.item_empty[i % ITEMS]);
+  };
 
   if (warp == 0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
@@ -250,38 +308,24 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto wait_all = [&](uint64_t *bar, uint32_t parity, uint32_t where) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns, where));
     };
-    while (ok && walk_next(wk, t, p)) {
-      const PlanPiece pc = wk.pc;
-      if (pc.t0 >= pc.t1) continue;
-      const PlanSeq s = t.seq[pc.b];
-      const int g = wk.group * p.group_heads + pc.g;
-      const int tok0 = pc.p * 2 * p.tq, tiles_q = s.n - tok0 > p.tq ? 2 : 1;
-      for (int x = 0; ok && x < tiles_q; ++x, ++qc) {
-        const int qs = qc & 1;
-        ok = wait_all(&t.q_empty[qs], ((qc >> 1) & 1) ^ 1, 0x51u);
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(&t.q_full[qs], p.tq * p.G * D * 2);
-          for (int i = 0; i < CH; ++i)
-            tma_load_3d(sQ + qs * TILE + i * CHUNK, &tmQ, &t.q_full[qs], i * 64, g * p.G,
-                        t.first[pc.b] + tok0 + x * p.tq);
-        }
-        if (ok) {
-          q_issued |= 1u << qs;
-          q_par = (q_par & ~(1u << qs)) | (((qc >> 1) & 1u) << qs);
-        }
-      }
-      // the page of this lane's box, one tile ahead; outside the tensor where there is none
-      auto page_of = [&](int j) -> int {
-        const int slot = j * BKV + box * rows;
-        if (!mine || slot >= s.L) return p.c.num_pages;
-        const int n = paged_page(p.c.table, p.c.table_stride, p.c.num_pages, pc.b, slot >> p.c.page_shift, p.status);
-        return n < 0 ? p.c.num_pages : n;
-      };
-      int next = page_of(pc.t0);
-      for (int j = pc.t0; ok && j < pc.t1; ++j, ++kc) {
+    // the page of this lane's box in tile j; outside the tensor where there is none
+    auto page_of = [&](int b, int L, int j) -> int {
+      const int slot = j * BKV + box * rows;
+      if (!mine || slot >= L) return p.c.num_pages;
+      const int n = paged_page(p.c.table, p.c.table_stride, p.c.num_pages, b, slot >> p.c.page_shift, p.status);
+      return n < 0 ? p.c.num_pages : n;
+    };
+    for (int i = 0; ok; ++i) {
+      const Item *it = take(i);
+      if (!it) break;
+      const int b = it->b, t0 = uniform(it->t0), t1 = uniform(it->t1), g = it->g, L = it->L;
+      const int row0 = it->first + it->tok0, tiles_q = uniform(it->two) ? 2 : 1;
+      give_back(i);
+      int next = t0 < t1 ? page_of(b, L, t0) : 0;  // one tile ahead
+      for (int j = t0; ok && j < t1; ++j, ++kc) {
         const int st = kc % STAGES, at = next, row = (j * BKV) & (page - 1);
         const uint32_t ph = (kc / STAGES) & 1;
-        if (j + 1 < pc.t1) next = page_of(j + 1);
+        if (j + 1 < t1) next = page_of(b, L, j + 1);
         const int off = st * TILE + ch * CHUNK + box * rows * 128;
         ok = wait_all(&t.k_empty[st], ph ^ 1u, 0x52u);
         if (!ok) break;
@@ -290,6 +334,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (mine) tma_load_4d(sK + off, &tmK, &t.k_full[st], ch * 64, g, row, at);
         k_issued |= 1u << st;
         k_par = (k_par & ~(1u << st)) | (ph << st);
+        // the unit's Q behind its first K tile: that place is free earlier
+        for (int x = 0; ok && j == t0 && x < tiles_q; ++x, ++qc) {
+          const int qs = qc & 1;
+          const uint32_t qph = (qc >> 1) & 1;
+          ok = wait_all(&t.q_empty[qs], qph ^ 1u, 0x51u);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&t.q_full[qs], p.tq * p.G * D * 2);
+            for (int e = 0; e < CH; ++e)
+              tma_load_3d(sQ + qs * TILE + e * CHUNK, &tmQ, &t.q_full[qs], e * 64, g * p.G, row0 + x * p.tq);
+          }
+          q_issued |= 1u << qs;
+          q_par = (q_par & ~(1u << qs)) | (qph << qs);
+        }
+        if (!ok) break;
         ok = wait_all(&t.v_empty[st], ph ^ 1u, 0x53u);
         if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&t.v_full[st], TILE);
@@ -355,16 +414,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       ++used[x];
       return true;
     };
-    while (ok && walk_next(wk, t, p)) {
-      const PlanPiece &pc = wk.pc;
-      const int t0 = uniform(pc.t0), n = uniform(pc.t1) - t0;
-      if (n <= 0) continue;
-      const PlanSeq s{uniform(t.seq[pc.b].n), uniform(t.seq[pc.b].L)};
-      const int tok0 = uniform(pc.p) * 2 * p.tq;
-      const bool two = s.n - tok0 > p.tq;
+    for (int item = 0; ok; ++item) {
+      const Item *it = take(item);
+      if (!it) break;
+      const int t0 = uniform(it->t0), n = uniform(it->t1) - t0, L = uniform(it->L);
+      const bool two = uniform(it->two) != 0;
       // tiles of x = 0 when it has a Q tile of its own
-      const int n_a = two ? max(min((plan_visible(s, tok0 + p.tq) + BKV - 1) / BKV - t0, n), 0) : 0;
-      const int fix = (s.L & (BKV - 1)) ? s.L / BKV - t0 : -1;  // the tile that warp 2 mends
+      const int n_a = max(min(uniform(it->a_end) - t0, n), 0);
+      give_back(item);
+      if (n <= 0) continue;
+      const int fix = (L & (BKV - 1)) ? L / BKV - t0 : -1;  // the tile that warp 2 mends
       bool fixed = fix < 0 || fix >= n;
       bool free_ = false;
       auto before_pv = [&](int i) -> bool {  // O free of the last unit, V of tile i mended
@@ -429,10 +488,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       // It takes part in every tile, so that its parity waits skip no phase.
       int kc = 0;
       bool ok = true;
-      while (ok && walk_next(wk, t, p)) {
-        const PlanPiece pc = wk.pc;
-        const int L = pc.t0 < pc.t1 ? t.seq[pc.b].L : 0, from = L & (BKV - 1);
-        for (int j = pc.t0; j < pc.t1; ++j, ++kc) {
+      for (int i = 0; ok; ++i) {
+        const Item *it = take(i);
+        if (!it) break;
+        const int t0 = it->t0, t1 = it->t1, L = it->L, from = L & (BKV - 1);
+        give_back(i);
+        for (int j = t0; j < t1; ++j, ++kc) {
           const int st = kc % STAGES;
           ok = __all_sync(0xffffffffu, mbar_wait(&t.v_full[st], (kc / STAGES) & 1, abort_flag, p.status, p.wait_ns,
                                                  0x5Au));
@@ -449,7 +510,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (lane == 0) mbar_arrive(&t.v_empty[st]);
         }
       }
+    } else if (lane == 0) {
+      walk(t, p);
     }
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HIGH));
     // ---------------- softmax: warps 4..7 x = 0, warps 8..11 x = 1
@@ -462,24 +526,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float c2 = p.scale_log2;
     uint32_t used = 0, joins = 0;  // tiles processed, exchanges with the other warpgroup
     bool ok = true;
-    while (ok && walk_next(wk, t, p)) {
-      // what outlives the key loop is read again from the Walk
+    for (int item = 0; ok; ++item) {
+      const Item *it = take(item);
+      if (!it) break;
+      // what is needed behind the key loop is read from the item again there
       int t0, t1, step, own_tiles, mask_from, lim;
       bool live, two;
       {
-        const PlanPiece &pc = wk.pc;
-        const PlanSeq s = t.seq[pc.b];
-        const int tok0 = pc.p * 2 * p.tq;
-        two = s.n - tok0 > p.tq;
+        const PlanSeq s{it->n, it->L};
+        const int tok0 = it->tok0;
+        two = it->two != 0;
         const int shift = two ? x * p.tq : 0;  // this tile's first token in the window
         live = rt < p.tq && tok0 + shift + rt < s.n;
         lim = live ? plan_visible(s, tok0 + shift + rt + 1) : 0;
         mask_from = plan_visible(s, tok0 + shift + 1);
-        t0 = pc.t0;
-        t1 = pc.t1;
+        t0 = it->t0;
+        t1 = it->t1;
         const int n = max(t1 - t0, 0);
         if (two) {
-          const int n_a = max(min((plan_visible(s, tok0 + p.tq) + BKV - 1) / BKV, t1) - t0, 0);
+          const int n_a = max(min(it->a_end, t1) - t0, 0);
           own_tiles = x ? n : n_a;
           step = 1;
         } else {
@@ -614,13 +679,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         f1 = ex2(b.x - top);
         l = a.y * f0 + b.y * f1;
       }
-      const PlanPiece &pc = wk.pc;
-      const int g = wk.group * p.group_heads + pc.g;
-      const int row = (two ? x * p.tq : 0) + rt;                   // token inside the window
-      const int tok = t.first[pc.b] + pc.p * 2 * p.tq + row;       // packed row
-      const int head = g * p.G + rh;
-      const int64_t part = (static_cast<int64_t>(wk.group) * gridDim.x + blockIdx.x) * 2 + pc.slot;
-      const bool whole = pc.whole != 0;
+      const int row = (two ? x * p.tq : 0) + rt;      // token inside the window
+      const int tok = it->first + it->tok0 + row;     // packed row
+      const int head = it->g * p.G + rh;
+      const int64_t part = it->part;
+      const bool whole = it->whole != 0;
+      give_back(item);
       // columns this warpgroup writes: all of its own O, or its half of the joined one
       const int c0 = two ? 0 : x * (D / 64), c1 = two ? D / 32 : (x + 1) * (D / 64);
       const bool first_wg = two || x == 0;
@@ -668,9 +732,9 @@ __global__ void __launch_bounds__(THREADS, 1)
               dst[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
                                   pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
           } else {
-            float4 *dst = reinterpret_cast<float4 *>(p.part_o + (part * SLOT_ROWS + row * p.G + rh) * D + c * 32);
+            float *dst = p.part_o + (part * SLOT_ROWS + row * p.G + rh) * D + c * 32;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) store_8(dst + 8 * q, v + 8 * q);
           }
         }
       }
@@ -702,13 +766,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Joins the pieces of the unit whose first cut is in front of range
 // blockIdx.x + 1 of group blockIdx.y: O = sum_i 2^(m_i - m) O_i / sum_i
-// 2^(m_i - m) l_i, the pieces in order, one warp per row.
-constexpr int JOIN_THREADS = 256;
+// 2^(m_i - m) l_i, the pieces in order, one warp per row.  Launched while the
+// attention still runs (its CTAs take the places of those that ended), and
+// waits for it.
+constexpr int JOIN_WARPS = 8;
 constexpr int JOIN_SPLIT = 8;  // CTAs per unit
 
 template <int D>
-__global__ void __launch_bounds__(JOIN_THREADS) paged_combine_kernel(const __grid_constant__ Params p, int ctas) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __grid_constant__ Params p, int ctas) {
   const int range = blockIdx.x + 1, group = blockIdx.y;
+  constexpr int E = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const PlanCut cut = p.cuts[group * ctas + range];
   if (!plan_first_cut(cut, range)) return;
   int first, n;
@@ -718,26 +786,47 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_combine_kernel(const __gri
   const int rows = min(w, n - tok0) * p.G;
   const int tiles = (plan_visible(s, tok0 + w) + BKV - 1) / BKV;
   const int lane = threadIdx.x & 31;
-  constexpr int E = D / 32;
-  for (int row = blockIdx.z * (JOIN_THREADS / 32) + (threadIdx.x >> 5); row < rows;
-       row += JOIN_SPLIT * (JOIN_THREADS / 32)) {
+  // where piece i of this unit lies, or -1 if it has no tile; `last`: whether it ends the unit
+  auto piece = [&](int i, bool &last) -> int64_t {
+    int rg, slot, off, end, t0, t1;
+    plan_piece_of(cut, range, i, rg, slot, off, end);
+    last = end == cut.c;
+    if (off == cut.c) return -1;
+    plan_tiles(off, end, cut.c, tiles, t0, t1);
+    return t0 < t1 ? ((static_cast<int64_t>(group) * ctas + rg) * 2 + slot) * SLOT_ROWS : -1;
+  };
+  for (int row = blockIdx.z * JOIN_WARPS + (threadIdx.x >> 5); row < rows; row += JOIN_SPLIT * JOIN_WARPS) {
     float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int i = 0, end = 0; end != cut.c; ++i) {
-      int rg, slot, off, t0, t1;
-      plan_piece_of(cut, range, i, rg, slot, off, end);
-      plan_tiles(off, end, cut.c, tiles, t0, t1);
-      if (t0 >= t1) continue;
-      const int64_t part = ((static_cast<int64_t>(group) * ctas + rg) * 2 + slot) * SLOT_ROWS + row;
-      const float2 ml = p.part_ml[part];
-      if (ml.x == -INFINITY) continue;  // this row sees nothing of the piece
-      const float mn = max_nan(m, ml.x), fa = m == -INFINITY ? 0.f : ex2(m - mn), fb = ex2(ml.x - mn);
-      const float *o = p.part_o + part * D + lane * E;
-      l = l * fa + ml.y * fb;
+    bool done = false;
+    for (int i0 = 0; !done; i0 += 32) {  // 32 pieces at a time: lane i has the statistics of piece i0 + i
+      bool last;
+      const int64_t at = piece(i0 + lane, last);
+      done = __any_sync(0xffffffffu, last);
+      const float2 ml = at >= 0 ? p.part_ml[at + row] : make_float2(-INFINITY, 0.f);
+      float top = ml.x;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(o[e], fb, acc[e] * fa);
+      for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float mn = max_nan(m, top), zero = mn == -INFINITY ? 0.f : mn;
+      const float keep = ex2(m - zero), f = ex2(ml.x - zero);
+      float part = ml.y * f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+      l = l * keep + part;
       m = mn;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] *= keep;
+      // pieces of which this row sees nothing are skipped: their O may be anything
+      uint32_t live = __ballot_sync(0xffffffffu, at >= 0 && ml.x != -INFINITY);
+      while (live) {
+        const int i = __ffs(live) - 1;
+        live &= live - 1;
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float *o = p.part_o + (__shfl_sync(0xffffffffu, at, i) + row) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(o[e], fi, acc[e]);
+      }
     }
     const int tok = first + tok0 + row / p.G, head = g * p.G + row % p.G;
     const bool none = plan_visible(s, tok0 + row / p.G + 1) == 0;
@@ -785,9 +874,7 @@ spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   note_launch();
   SPTS_CUDA_TRY(cudaGetLastError());
   if (ctas > 1) {
-    paged_combine_kernel<D><<<dim3(ctas - 1, p.groups, JOIN_SPLIT), JOIN_THREADS, 0, s>>>(p, ctas);
-    note_launch();
-    SPTS_CUDA_TRY(cudaGetLastError());
+    SPTS_TRY(launch_behind(paged_combine_kernel<D>, dim3(ctas - 1, p.groups, JOIN_SPLIT), 32 * JOIN_WARPS, s, p, ctas));
   }
   return SPTS_OK;
 }

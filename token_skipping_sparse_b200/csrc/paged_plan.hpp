@@ -4,9 +4,9 @@
 //
 // Work is counted in key slots.  A unit is a window of w new tokens of one
 // sequence (two Q tiles of w / 2 tokens) and one KV head; window p of a
-// sequence with n new tokens behind `base` earlier ones costs
-// base + (p + 1) w slots, which is what its last token sees (a little more in
-// the last window), so the cost of the first p windows has a closed form and
+// sequence with n new tokens behind others costs base + (p + 1) w slots: what
+// its last token sees (a little more in the last window) and a constant for
+// what a unit costs beyond its tiles, so the cost of the first p windows has a closed form and
 // no list of units is needed.  Units are ordered by (head group, sequence,
 // window, head); a group's units, end to end, are cut into equal ranges, one
 // per CTA, wherever the cuts fall.  A unit that a cut divides is put together
@@ -24,6 +24,15 @@
 namespace spts {
 
 constexpr int PLAN_TILE = 128;  // key slots of one tile
+// What a unit costs beyond its tiles (its Q, the end of its pipeline, its
+// output), in key slots: PLAN_ONE with one Q tile, PLAN_TWO with two.
+#ifndef SPTS_PLAN_ONE
+#define SPTS_PLAN_ONE 128
+#endif
+#ifndef SPTS_PLAN_TWO
+#define SPTS_PLAN_TWO 512
+#endif
+constexpr int PLAN_ONE = SPTS_PLAN_ONE, PLAN_TWO = SPTS_PLAN_TWO;
 
 SPTS_HD int plan_min(int a, int b) { return a < b ? a : b; }
 SPTS_HD int plan_max(int a, int b) { return a > b ? a : b; }
@@ -33,7 +42,10 @@ struct PlanSeq {
 };
 
 SPTS_HD int plan_windows(int n, int w) { return (n + w - 1) / w; }
-SPTS_HD int plan_base(const PlanSeq &s) { return plan_max(s.L - s.n, 0); }
+// What every window of a sequence costs besides its own tokens.
+SPTS_HD int plan_base(const PlanSeq &s, int w) {
+  return plan_max(s.L - s.n, 0) + (s.n > w / 2 ? PLAN_TWO : PLAN_ONE);
+}
 // Cost of the first p windows of a sequence, for one head.
 SPTS_HD int64_t plan_cost(int base, int p, int w) {
   return static_cast<int64_t>(p) * base + static_cast<int64_t>(w) * p * (p + 1) / 2;
@@ -74,7 +86,7 @@ SPTS_HD int plan_ranges(int64_t total, int ctas) {
 
 // y: position inside the sequence's units of one head group of `heads` heads.
 SPTS_HD PlanUnit plan_locate(const PlanSeq &s, int w, int heads, int64_t y) {
-  const int base = plan_base(s);
+  const int base = plan_base(s, w);
   int lo = 0, hi = plan_windows(s.n, w) - 1;  // the window, by its first position
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -150,7 +162,7 @@ SPTS_HD int plan_next(PlanCursor &cur, const PlanSeq *seq, int B, int w, int hea
         while (cur.b < B && seq[cur.b].n <= 0);
       }
     }
-    if (cur.b < B) cur.c = plan_base(seq[cur.b]) + (cur.p + 1) * w;
+    if (cur.b < B) cur.c = plan_base(seq[cur.b], w) + (cur.p + 1) * w;
   } else {
     cur.off += take;
   }
@@ -172,14 +184,16 @@ SPTS_HD int plan_first_cut(const PlanCut &cut, int r) {
 }
 
 // Piece i of the unit whose first cut is in front of range r: the range that
-// computed it, its slot there, and its [off, end) in the unit.
+// computed it, its slot there, and its [off, end) in the unit (empty, at the
+// unit's end, past its last piece).
 SPTS_HD void plan_piece_of(const PlanCut &cut, int r, int i, int &range, int &slot, int &off, int &end) {
-  const int64_t start = plan_cut(cut.total, cut.nr, r) - cut.off;
+  const int64_t start = plan_cut(cut.total, cut.nr, r) - cut.off, c = cut.c;
   range = r - 1 + i;
   slot = i == 0 ? 1 : 0;
-  off = i == 0 ? 0 : static_cast<int>(plan_cut(cut.total, cut.nr, range) - start);
+  const int64_t o = i == 0 ? 0 : plan_cut(cut.total, cut.nr, range) - start;
   const int64_t e = plan_cut(cut.total, cut.nr, range + 1) - start;
-  end = e < cut.c ? static_cast<int>(e) : cut.c;
+  off = static_cast<int>(o < c ? o : c);
+  end = static_cast<int>(e < c ? e : c);
 }
 
 }  // namespace spts
