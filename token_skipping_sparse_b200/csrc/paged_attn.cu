@@ -22,7 +22,8 @@
 //   warp 1      MMA: S_x = Q_x K^T into TMEM, then O_x += P_x V with P_x read
 //               from TMEM; the loop runs across units without a drain;
 //   warp 2      zeroes the V rows behind the sequence's last slot in its last
-//               tile: they may hold anything, and 0 x NaN is NaN;
+//               tile (they may hold anything, and 0 x NaN is NaN), between
+//               that tile's load and the MMA warp;
 //   warp 3      walks the plan and hands the pieces to the other warps through
 //               a ring of ITEMS places, ahead of them;
 //   warps 4..7, 8..11  softmax, one thread per row, one warpgroup per S_x.
@@ -90,7 +91,7 @@ struct Tail {  // shared memory behind the tiles
   int first[MAX_SEQ];
   float2 xchg[2][2][128];  // by turns: a warpgroup without a tile may be one piece ahead
   uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t v_fix[4];  // per stage, so that warp 2 cannot be two phases ahead of the MMA warp
+  uint64_t v_raw[4];  // instead of v_full where a tile's V goes through warp 2
   uint64_t s_full[2], p_ready[4], o_done[2], o_free, x_full, drain;
   uint64_t item_full[ITEMS], item_empty[ITEMS];
   Item item[ITEMS];
@@ -160,7 +161,7 @@ __device__ __forceinline__ void walk(Tail &t, const Params &p) {
   bool ok = true;
   auto place = [&]() -> Item * {  // the next free place of the ring
     const int i = count % ITEMS;
-    ok = mbar_wait(&t.item_empty[i], ((count / ITEMS) & 1) ^ 1, abort_flag, p.status, p.wait_ns, 0x50u);
+    ok = mbar_wait_long(&t.item_empty[i], ((count / ITEMS) & 1) ^ 1, abort_flag, p.status, p.wait_ns, 0x50u);
     return &t.item[i];
   };
   for (int group = 0; ok && group < p.groups; ++group) {
@@ -262,8 +263,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&t.k_full[s], 1);
       mbar_init(&t.k_empty[s], 1);
       mbar_init(&t.v_full[s], 1);
-      mbar_init(&t.v_empty[s], 2);  // the MMA warp's commit and warp 2
-      mbar_init(&t.v_fix[s], 32);
+      mbar_init(&t.v_empty[s], 1);
+      mbar_init(&t.v_raw[s], 1);
     }
     mbar_init(&t.o_free, 256);
     mbar_init(&t.x_full, 256);
@@ -286,8 +287,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   // The i-th item for this warp, or null behind the last one (or on the way
   // out); give_back lets warp 3 reuse its place.
   auto take = [&](int i) -> const Item * {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(&t.item_full[i % ITEMS], (i / ITEMS) & 1, abort_flag, p.status,
-                                                      p.wait_ns, 0x5Fu));
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_long(&t.item_full[i % ITEMS], (i / ITEMS) & 1, abort_flag,
+                                                           p.status, p.wait_ns, 0x5Fu));
     const Item *it = &t.item[i % ITEMS];
     return ok && uniform(it->more) ? it : nullptr;
   };
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool mine = lane < boxes * CH;
     const int box = lane / CH, ch = lane % CH;
     int qc = 0, kc = 0;  // Q tiles and K/V tiles loaded so far
-    uint32_t k_issued = 0, k_par = 0, v_issued = 0, v_par = 0, q_issued = 0, q_par = 0;
+    uint32_t k_issued = 0, k_par = 0, v_issued = 0, v_par = 0, v_raw = 0, raw_par = 0, q_issued = 0, q_par = 0;
     bool ok = true;
     auto wait_all = [&](uint64_t *bar, uint32_t parity, uint32_t where) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns, where));
@@ -351,11 +352,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         ok = wait_all(&t.v_empty[st], ph ^ 1u, 0x53u);
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&t.v_full[st], TILE);
+        const bool tail = (L & (BKV - 1)) && j == L / BKV;
+        uint64_t *bar = tail ? &t.v_raw[st] : &t.v_full[st];
+        if (lane == 0) mbar_arrive_expect_tx(bar, TILE);
         __syncwarp();
-        if (mine) tma_load_4d(sV + off, &tmV, &t.v_full[st], ch * 64, g, row, at);
+        if (mine) tma_load_4d(sV + off, &tmV, bar, ch * 64, g, row, at);
         v_issued |= 1u << st;
+        v_raw = (v_raw & ~(1u << st)) | (static_cast<uint32_t>(tail) << st);
         v_par = (v_par & ~(1u << st)) | (ph << st);
+        raw_par ^= static_cast<uint32_t>(tail) << st;  // phases of v_raw used so far
       }
     }
     if (*abort_flag && lane == 0) {
@@ -363,7 +368,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (q_issued & (1u << i)) mbar_drain(&t.q_full[i], (q_par >> i) & 1u, p.status);
       for (int i = 0; i < STAGES; ++i) {
         if (k_issued & (1u << i)) mbar_drain(&t.k_full[i], (k_par >> i) & 1u, p.status);
-        if (v_issued & (1u << i)) mbar_drain(&t.v_full[i], (v_par >> i) & 1u, p.status);
+        if (v_issued & (1u << i)) {  // the stage's last copy
+          if (v_raw & (1u << i)) mbar_drain(&t.v_raw[i], ((raw_par >> i) & 1u) ^ 1u, p.status);
+          else mbar_drain(&t.v_full[i], (v_par >> i) & 1u, p.status);
+        }
       }
     }
     __syncwarp();
@@ -376,7 +384,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns, where));
     };
     int qc = 0, kc = 0, units = 0;
-    uint32_t fix_par = 0;  // per stage, the parity of its next mended tile
     uint32_t used[2] = {0, 0};  // PVs issued per x
     bool ok = true;
     // S_x of the K tile in ring place `k` with the Q tile in place `q`, the q-th and k-th loaded
@@ -417,27 +424,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int item = 0; ok; ++item) {
       const Item *it = take(item);
       if (!it) break;
-      const int t0 = uniform(it->t0), n = uniform(it->t1) - t0, L = uniform(it->L);
+      const int t0 = uniform(it->t0), n = uniform(it->t1) - t0;
       const bool two = uniform(it->two) != 0;
       // tiles of x = 0 when it has a Q tile of its own
       const int n_a = max(min(uniform(it->a_end) - t0, n), 0);
       give_back(item);
       if (n <= 0) continue;
-      const int fix = (L & (BKV - 1)) ? L / BKV - t0 : -1;  // the tile that warp 2 mends
-      bool fixed = fix < 0 || fix >= n;
-      bool free_ = false;
-      auto before_pv = [&](int i) -> bool {  // O free of the last unit, V of tile i mended
-        if (!free_) {
-          free_ = true;
-          if (!wait_all(&t.o_free, (units & 1) ^ 1, 0x58u)) return false;
-        }
-        if (!fixed && i == fix) {
-          fixed = true;
-          const int st = (kc + i) % STAGES;
-          if (!wait_all(&t.v_fix[st], (fix_par >> st) & 1u, 0x59u)) return false;
-          fix_par ^= 1u << st;
-        }
-        return true;
+      bool first_pv = true;
+      auto o_is_free = [&]() -> bool {  // before the piece's first PV: the softmax has read the last piece's O
+        const bool first = first_pv;
+        first_pv = false;
+        return !first || wait_all(&t.o_free, (units & 1) ^ 1, 0x58u);
       };
       if (two) {
         for (int x = 0; ok && x < 2; ++x) {
@@ -451,7 +448,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int x = 0; ok && x < 2; ++x) {
             const int nx = x ? n : n_a;
             if (i >= nx) continue;
-            ok = before_pv(i) && issue_pv(x, kc + i, i == 0);
+            ok = o_is_free() && issue_pv(x, kc + i, i == 0);
             if (ok && i + 1 < nx) {
               ok = issue_s(x, qc + x, kc + i + 1);
               if (ok && i + 2 == nx) tc_commit_w(&t.q_empty[(qc + x) & 1]);
@@ -465,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       } else {
         for (int i = -2; ok && i < n; ++i) {
           if (i >= 0) {
-            ok = before_pv(i) && issue_pv(i & 1, kc + i, i < 2);
+            ok = o_is_free() && issue_pv(i & 1, kc + i, i < 2);
             if (ok) tc_commit_w(&t.v_empty[(kc + i) % STAGES]);
           }
           if (ok && i + 2 < n) {
@@ -485,30 +482,30 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
     if (warp == 2) {
-      // It takes part in every tile, so that its parity waits skip no phase.
       int kc = 0;
+      uint32_t par = 0;  // per stage, the parity of its next such tile
       bool ok = true;
       for (int i = 0; ok; ++i) {
         const Item *it = take(i);
         if (!it) break;
-        const int t0 = it->t0, t1 = it->t1, L = it->L, from = L & (BKV - 1);
+        const int n = it->t1 - it->t0, L = it->L, from = L & (BKV - 1), at = L / BKV - it->t0;
         give_back(i);
-        for (int j = t0; j < t1; ++j, ++kc) {
-          const int st = kc % STAGES;
-          ok = __all_sync(0xffffffffu, mbar_wait(&t.v_full[st], (kc / STAGES) & 1, abort_flag, p.status, p.wait_ns,
-                                                 0x5Au));
+        if (from && at >= 0 && at < n) {
+          const int st = (kc + at) % STAGES;
+          ok = __all_sync(0xffffffffu, mbar_wait_long(&t.v_raw[st], (par >> st) & 1u, abort_flag, p.status,
+                                                      p.wait_ns, 0x5Au));
           if (!ok) break;
-          if (from && j == L / BKV) {
-            // a row's 128 bytes stay its own under the swizzle
-            for (int ch = 0; ch < CH; ++ch) {
-              uint4 *rows = reinterpret_cast<uint4 *>(sV + st * TILE + ch * CHUNK + from * 128);
-              for (int e = lane; e < (BKV - from) * 8; e += 32) rows[e] = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            mbar_arrive(&t.v_fix[st]);
+          par ^= 1u << st;
+          // a row's 128 bytes stay its own under the swizzle
+          for (int ch = 0; ch < CH; ++ch) {
+            uint4 *rows = reinterpret_cast<uint4 *>(sV + st * TILE + ch * CHUNK + from * 128);
+            for (int e = lane; e < (BKV - from) * 8; e += 32) rows[e] = make_uint4(0, 0, 0, 0);
           }
-          if (lane == 0) mbar_arrive(&t.v_empty[st]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&t.v_full[st]);
         }
+        kc += max(n, 0);
       }
     } else if (lane == 0) {
       walk(t, p);

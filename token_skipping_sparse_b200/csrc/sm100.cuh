@@ -89,6 +89,30 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
   }
 }
 
+// As mbar_wait, for warps that wait long beside busy ones: the thread sleeps in
+// the wait for up to ~20 us at a time instead of polling.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                               uint32_t *status, uint64_t limit_ns, uint32_t where) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      *abort_flag = 1;
+      raise_status(status, SPTS_DEV_TIMEOUT, where);
+      return false;
+    }
+  }
+}
+
 // Drain wait used on the abort path: fixed limit, no abort check.
 __device__ __forceinline__ bool mbar_drain(uint64_t *bar, uint32_t parity, uint32_t *status) {
   const uint64_t t0 = globaltimer_ns();
