@@ -274,8 +274,8 @@ def test_paged_cache_calls_want_cuda_tensors_of_the_right_kind():
         S.spts_paged_attention(k[0], k, k, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
                                torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError, match="page_table"):
-        S._lib._paged(k, k, torch.zeros(1, 1), torch.zeros(1, dtype=torch.int32))
+        S._lib._paged(k, k, torch.zeros(1, 1), torch.zeros(1, dtype=torch.int32), k.device)
     with pytest.raises(ValueError, match="alike"):
-        S._lib._paged(k, k[..., :32], torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+        S._lib._paged(k, k[..., :32], torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), k.device)
     with pytest.raises(ValueError, match="per sequence"):
-        S._lib._paged(k, k, torch.zeros(2, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+        S._lib._paged(k, k, torch.zeros(2, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), k.device)

@@ -10,6 +10,7 @@ arithmetic runs in the library's CUDA kernels; there is no fallback path.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 import threading
 
@@ -384,61 +385,84 @@ def spts_inject_salience(k, q_probe, rows, shift):
 
 
 # ---------------------------------------------------------------- the paged key/value cache
+# What the library cannot see behind a pointer (types, devices, strides) is
+# checked here: in one expression each, since a step of decoding is short, and
+# in words only once it has failed.
+_BF, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _want(t, dtype, dims, device, what):
-    """What the library cannot see behind a pointer: type, rank, device."""
+    """Type, rank and device of a tensor."""
     if t.dtype != dtype or t.dim() != dims or t.device != device:
         raise ValueError(f"{what}: need a {dims}-dimensional {dtype} tensor on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t
 
 
-def _inner(t, what):
-    """Row stride of packed tokens whose heads lie as in a contiguous tensor."""
-    _, H, d = t.shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d):
+def _packed(t, dev, what):
+    """Row stride of packed tokens [T, H, d] whose heads lie as in a contiguous tensor."""
+    if t.dtype is not _BF or t.dim() != 3 or t.device != dev:
+        _want(t, _BF, 3, dev, what)
+    T, H, d = t.shape
+    row, head, col = t.stride()
+    if col != 1 or (head != d and H > 1):
         raise ValueError(f"{what}: heads and columns must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else H * d
+    return row if T > 1 else H * d
 
 
-def _row_stride(t, what):
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+def _table_stride(t, what):
+    row, col = t.stride()
+    if col != 1 and t.shape[1] > 1:
         raise ValueError(f"{what}: entries of a row must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[-1]
+    return row if t.shape[0] > 1 else t.shape[1]
 
 
-def _score_stride(t, what):
-    """Stride between the rows [b, hs] of a weights tensor."""
-    B, Hs, n = t.shape
-    row = t.stride(1) if Hs > 1 else t.stride(0) if B > 1 else n
-    if (n > 1 and t.stride(2) != 1) or (B > 1 and t.stride(0) != Hs * row):
-        raise ValueError(f"{what}: need evenly spaced rows of contiguous entries")
-    return row
-
-
-def _paged(k_pages, v_pages, page_table, seq_lens):
-    dev = k_pages.device
-    _want(k_pages, torch.bfloat16, 4, dev, "k_pages")
-    _want(v_pages, torch.bfloat16, 4, dev, "v_pages")
-    _want(page_table, torch.int32, 2, dev, "page_table")
-    _want(seq_lens, torch.int32, 1, dev, "seq_lens")
-    n, page, Hkv, d = k_pages.shape
-    inner = (Hkv * d, d, 1)
-    if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() or \
-            any(k > 1 and s != want for k, s, want in zip(k_pages.shape[1:], k_pages.stride()[1:], inner)):
+def _paged(k_pages, v_pages, page_table, seq_lens, dev):
+    if not (k_pages.dtype is _BF and v_pages.dtype is _BF and page_table.dtype is _I32 and seq_lens.dtype is _I32 and
+            k_pages.dim() == 4 and page_table.dim() == 2 and seq_lens.dim() == 1 and k_pages.device == dev and
+            v_pages.device == dev and page_table.device == dev and seq_lens.device == dev):
+        _want(k_pages, _BF, 4, dev, "k_pages")
+        _want(v_pages, _BF, 4, dev, "v_pages")
+        _want(page_table, _I32, 2, dev, "page_table")
+        _want(seq_lens, _I32, 1, dev, "seq_lens")
+    n, page, Hkv, d = shape = k_pages.shape
+    st = k_pages.stride()
+    if v_pages.shape != shape or v_pages.stride() != st or \
+            (st[1:] != (Hkv * d, d, 1) and any(k > 1 and x != y for k, x, y in zip(shape[1:], st[1:], (Hkv * d, d, 1)))):
         raise ValueError("k_pages and v_pages must be alike, and contiguous inside a page")
-    B = seq_lens.shape[0]
-    if page_table.shape[0] != B or (B > 1 and seq_lens.stride(0) != 1):
+    rows, width = page_table.shape
+    row, col = page_table.stride()
+    B, = seq_lens.shape
+    if rows != B or (B > 1 and seq_lens.stride(0) != 1) or (col != 1 and width > 1):
         raise ValueError("page_table and seq_lens need one row and one contiguous entry per sequence")
-    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), n, k_pages.stride(0) if n > 1 else 0, page, B,
-                      page_table.data_ptr(), page_table.shape[1], _row_stride(page_table, "page_table"),
-                      seq_lens.data_ptr())
+    c = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), n, st[0] if n > 1 else 0, page, B, page_table.data_ptr(),
+                   width, row if B > 1 else width, seq_lens.data_ptr())
+    c.Hkv, c.d = Hkv, d
+    return c
 
 
-def _offsets(cu, B, dev, what):
-    _want(cu, torch.int32, 1, dev, what)
-    if cu.shape[0] != B + 1 or cu.stride(0) != 1:
-        raise ValueError(f"{what}: need B + 1 contiguous offsets")
-    return ptr(cu)
+def _vector(t, n, dev, what):
+    """Address of n contiguous int32 entries."""
+    if t.dtype is not _I32 or t.dim() != 1 or t.device != dev or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        _want(t, _I32, 1, dev, what)
+        raise ValueError(f"{what}: need {n} contiguous entries, got {tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _scores(weights, c, Hkv, dev, what):
+    """(Hs, stride between rows [b, hs], slots) of a weights tensor."""
+    if weights.dtype is not _F32 or weights.dim() != 3 or weights.device != dev:
+        _want(weights, _F32, 3, dev, what)
+    B, Hs, n = weights.shape
+    sb, sh, sn = weights.stride()
+    row = sh if Hs > 1 else sb if B > 1 else n
+    if B != c.B or Hs not in (1, Hkv):
+        raise ValueError(f"{what}: need [B, 1 or Hkv, slots], got {tuple(weights.shape)}")
+    if (n > 1 and sn != 1) or (B > 1 and sb != Hs * row):
+        raise ValueError(f"{what}: need evenly spaced rows of contiguous entries")
+    return Hs, row, n
 
 
 def _own_ws(ws, nbytes, dev):
@@ -451,123 +475,123 @@ def _own_ws(ws, nbytes, dev):
     return workspace(nbytes, dev)
 
 
-def _on_device(fn):
-    """Runs a cache call with the device of its first tensor current, so that
-    its launches, stream and workspace are that device's."""
-    import functools
-
-    @functools.wraps(fn)
-    def call(first, *args, **kw):
-        if first.device.type != "cuda":
-            raise ValueError(f"{fn.__name__}: tensors must be on a CUDA device, got {first.device}")
-        if first.device.index == torch.cuda.current_device():
-            return fn(first, *args, **kw)
-        with torch.cuda.device(first.device):
-            return fn(first, *args, **kw)
-    return call
+def _elsewhere(dev, who):
+    """Whether tensors on dev need another device made current first: a call's
+    launches, stream and workspace are those of its tensors' device."""
+    if dev.type != "cuda":
+        raise ValueError(f"{who}: tensors must be on a CUDA device, got {dev}")
+    return dev.index != torch.cuda.current_device()
 
 
-@_on_device
+@functools.lru_cache(maxsize=256)
+def _bf16_desc(Hq, Hkv, d, scale=0.0):
+    return AttnDesc(BF16, Hq, Hkv, d, scale)
+
+
+@functools.lru_cache(maxsize=1024)
+def _attention_ws_bytes(Hq, Hkv, d, B, page, max_pages, T, weights):
+    c = PagedCache(page_size=page, B=B, max_pages=max_pages)
+    return int(lib.spts_paged_attention_workspace(C.byref(_bf16_desc(Hq, Hkv, d)), C.byref(c), T, weights))
+
+
 def spts_cache_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, cu_new, pos=None, theta=500000.0, ws=None):
     """Writes packed new tokens' K (turned by RoPE at pos, if given) and V [T, Hkv, d] to the last slots of their
     sequences; seq_lens counts them already."""
     dev = k_new.device
-    c = _paged(_want(k_pages, torch.bfloat16, 4, dev, "k_pages"), v_pages, page_table, seq_lens)
-    T, Hkv, d = _want(k_new, torch.bfloat16, 3, dev, "k_new").shape
-    if _want(v_new, torch.bfloat16, 3, dev, "v_new").shape != k_new.shape or (Hkv, d) != tuple(k_pages.shape[2:]):
-        raise ValueError("k_new, v_new and the pages must agree in heads and head dim")
-    if pos is not None and (_want(pos, torch.int32, 1, dev, "pos").shape[0] != T or (T > 1 and pos.stride(0) != 1)):
-        raise ValueError("pos: need one contiguous position per new token")
-    a = AttnDesc(BF16, Hkv, Hkv, d, 0.0)
+    if _elsewhere(dev, "spts_cache_append"):
+        with torch.cuda.device(dev):
+            return spts_cache_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, cu_new, pos, theta, ws)
+    k_stride, v_stride = _packed(k_new, dev, "k_new"), _packed(v_new, dev, "v_new")
+    T, Hkv, d = shape = k_new.shape
+    c = _paged(k_pages, v_pages, page_table, seq_lens, dev)
+    if v_new.shape != shape or Hkv != c.Hkv or d != c.d:
+        raise ValueError("k_new, v_new and the pages must agree in tokens, heads and head dim")
+    cu, at = _vector(cu_new, c.B + 1, dev, "cu_new"), None if pos is None else _vector(pos, T, dev, "pos")
     ws = _own_ws(ws, 256, dev)
-    check(lib.spts_cache_append(C.byref(a), C.byref(c), ptr(k_new), _inner(k_new, "k_new"), ptr(v_new),
-                                _inner(v_new, "v_new"), _offsets(cu_new, c.B, dev, "cu_new"), T, ptr(pos), theta,
-                                ptr(ws), stream_ptr()))
-
-
-def _weights_arg(weights, c, Hkv, dev, what):
-    B, Hs, n = _want(weights, torch.float32, 3, dev, what).shape
-    if B != c.B or Hs not in (1, Hkv):
-        raise ValueError(f"{what}: need [B, 1 or Hkv, slots]")
-    return Hs, _score_stride(weights, what), n
+    check(lib.spts_cache_append(C.byref(_bf16_desc(Hkv, Hkv, d)), C.byref(c), k_new.data_ptr(), k_stride,
+                                v_new.data_ptr(), v_stride, cu, T, at, theta, ws.data_ptr(), _raw_stream(dev.index)))
 
 
 def spts_paged_attention_workspace(q, k_pages, v_pages, page_table, seq_lens, weights=False):
     """Bytes of workspace that spts_paged_attention needs for these arguments."""
     T, Hq, d = q.shape
-    a = AttnDesc(BF16, Hq, k_pages.shape[2], d, 0.0)
-    c = _paged(k_pages, v_pages, page_table, seq_lens)
-    return int(lib.spts_paged_attention_workspace(C.byref(a), C.byref(c), T, 1 if weights else 0))
+    return _attention_ws_bytes(Hq, k_pages.shape[2], d, seq_lens.shape[0], k_pages.shape[1], page_table.shape[1], T,
+                               1 if weights else 0)
 
 
-@_on_device
 def spts_paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_q, scale=None, out=None, lse=False,
                          weights=None, ws=None):
     """Attention of packed new tokens q [T, Hq, d] over the paged cache, causal inside each sequence.
     Returns o [T, Hq, d], with lse=True (o, lse [T, Hq]); `weights` [B, Hkv or 1, slots] is added to in place."""
     dev = q.device
-    c = _paged(_want(k_pages, torch.bfloat16, 4, dev, "k_pages"), v_pages, page_table, seq_lens)
-    T, Hq, d = _want(q, torch.bfloat16, 3, dev, "q").shape
-    Hkv = k_pages.shape[2]
-    if d != k_pages.shape[3]:
+    if _elsewhere(dev, "spts_paged_attention"):
+        with torch.cuda.device(dev):
+            return spts_paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_q, scale, out, lse, weights, ws)
+    q_stride = _packed(q, dev, "q")
+    T, Hq, d = shape = q.shape
+    c = _paged(k_pages, v_pages, page_table, seq_lens, dev)
+    Hkv = c.Hkv
+    if d != c.d:
         raise ValueError("q and the pages must agree in head dim")
-    a = AttnDesc(BF16, Hq, Hkv, d, 0.0 if scale is None else float(scale))
     if out is None:
-        o = torch.empty(T, Hq, d, dtype=torch.bfloat16, device=dev)
+        o, o_stride = q.new_empty(shape), 0
     else:
-        o = out
-        if _want(o, torch.bfloat16, 3, dev, "out").shape != q.shape:
+        o, o_stride = out, _packed(out, dev, "out")
+        if o.shape != shape:
             raise ValueError("out: need q's shape")
-    e = torch.empty(T, Hq, dtype=torch.float32, device=dev) if lse else None
+    e = q.new_empty((T, Hq), dtype=_F32) if lse else None
     Hs = stride = 0
     if weights is not None:
-        Hs, stride, n = _weights_arg(weights, c, Hkv, dev, "weights")
+        Hs, stride, n = _scores(weights, c, Hkv, dev, "weights")
         if n < c.max_pages * c.page_size:
             raise ValueError("weights: need a slot for every slot of a page table row")
-    ws = _own_ws(ws, lib.spts_paged_attention_workspace(C.byref(a), C.byref(c), T, 0 if weights is None else 1), dev)
-    check(lib.spts_paged_attention(C.byref(a), C.byref(c), ptr(q), _inner(q, "q"), _offsets(cu_q, c.B, dev, "cu_q"), T,
-                                   ptr(o), _inner(o, "out"), ptr(e), ptr(weights), Hs, stride, ptr(ws), ws.numel(),
-                                   stream_ptr()))
+    ws = _own_ws(ws, _attention_ws_bytes(Hq, Hkv, d, c.B, c.page_size, c.max_pages, T, 0 if weights is None else 1), dev)
+    a = _bf16_desc(Hq, Hkv, d, 0.0 if scale is None else float(scale))
+    check(lib.spts_paged_attention(C.byref(a), C.byref(c), q.data_ptr(), q_stride, _vector(cu_q, c.B + 1, dev, "cu_q"),
+                                   T, o.data_ptr(), o_stride, None if e is None else e.data_ptr(),
+                                   None if weights is None else weights.data_ptr(), Hs, stride, ws.data_ptr(),
+                                   ws.numel(), _raw_stream(dev.index)))
     return (o, e) if lse else o
 
 
 def spts_cache_evict_workspace(k_pages, v_pages, page_table, seq_lens, weights, keep):
     """Bytes of workspace that spts_cache_evict needs for these arguments."""
-    c = _paged(k_pages, v_pages, page_table, seq_lens)
+    c = PagedCache(page_size=k_pages.shape[1], B=seq_lens.shape[0], max_pages=page_table.shape[1])
     return int(lib.spts_cache_evict_workspace(C.byref(c), weights.shape[1], keep))
 
 
-@_on_device
 def spts_cache_evict(k_pages, v_pages, page_table, seq_lens, weights, keep, sink=0, recent=0, dst_table=None,
                      weights_out=None, new_lens=None, kept=False, ws=None):
     """Keeps `keep` tokens of every longer sequence by accumulated weight.  With dst_table the kept rows go to its
     pages, without it the cache and (unless weights_out is given) the weights are compacted in place.
     Returns (new_lens, weights_out), with kept=True also the kept slots [B, Hs, keep] (-1 behind the last)."""
     dev = k_pages.device
-    c = _paged(k_pages, v_pages, page_table, seq_lens)
-    Hkv, d = k_pages.shape[2:]
-    Hs, stride, n = _weights_arg(weights, c, Hkv, dev, "weights")
+    if _elsewhere(dev, "spts_cache_evict"):
+        with torch.cuda.device(dev):
+            return spts_cache_evict(k_pages, v_pages, page_table, seq_lens, weights, keep, sink, recent, dst_table,
+                                    weights_out, new_lens, kept, ws)
+    c = _paged(k_pages, v_pages, page_table, seq_lens, dev)
+    Hkv, d = c.Hkv, c.d
+    Hs, stride, n = _scores(weights, c, Hkv, dev, "weights")
     if n < c.max_pages * c.page_size:
         raise ValueError("weights: need a slot for every slot of a page table row")
-    dst = page_table if dst_table is None else _want(dst_table, torch.int32, 2, dev, "dst_table")
+    dst = page_table if dst_table is None else _want(dst_table, _I32, 2, dev, "dst_table")
     if dst.shape[0] != c.B:
         raise ValueError("dst_table: need one row per sequence")
     if weights_out is None:
-        weights_out = weights if dst_table is None else torch.empty(
-            c.B, Hs, dst.shape[1] * c.page_size, dtype=torch.float32, device=dev)
-    Ho, out_stride, m = _weights_arg(weights_out, c, Hkv, dev, "weights_out")
+        weights_out = weights if dst_table is None else weights.new_empty((c.B, Hs, dst.shape[1] * c.page_size))
+    Ho, out_stride, m = _scores(weights_out, c, Hkv, dev, "weights_out")
     if Ho != Hs or m != out_stride:
         raise ValueError("weights_out: need contiguous rows, as many as weights has")
     if new_lens is None:
-        new_lens = torch.empty(c.B, dtype=torch.int32, device=dev)
-    elif _want(new_lens, torch.int32, 1, dev, "new_lens").shape[0] != c.B or (c.B > 1 and new_lens.stride(0) != 1):
-        raise ValueError("new_lens: need one contiguous entry per sequence")
-    idx = torch.empty(c.B, Hs, keep, dtype=torch.int32, device=dev) if kept else None
-    a = AttnDesc(BF16, Hkv, Hkv, d, 0.0)
+        new_lens = seq_lens.new_empty(c.B)
+    idx = seq_lens.new_empty((c.B, Hs, keep)) if kept else None
     ws = _own_ws(ws, lib.spts_cache_evict_workspace(C.byref(c), Hs, keep), dev)
-    check(lib.spts_cache_evict(C.byref(a), C.byref(c), ptr(weights), Hs, stride, keep, sink, recent, ptr(dst),
-                               dst.shape[1], _row_stride(dst, "dst_table"), ptr(weights_out), out_stride,
-                               ptr(new_lens), ptr(idx), ptr(ws), ws.numel(), stream_ptr()))
+    check(lib.spts_cache_evict(C.byref(_bf16_desc(Hkv, Hkv, d)), C.byref(c), weights.data_ptr(), Hs, stride, keep, sink,
+                               recent, dst.data_ptr(), dst.shape[1], _table_stride(dst, "dst_table"),
+                               weights_out.data_ptr(), out_stride, _vector(new_lens, c.B, dev, "new_lens"),
+                               None if idx is None else idx.data_ptr(), ws.data_ptr(), ws.numel(),
+                               _raw_stream(dev.index)))
     return (new_lens, weights_out, idx) if kept else (new_lens, weights_out)
 
 

@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <utility>
 
@@ -31,7 +32,8 @@ struct PagedView {
 constexpr uint32_t kSitePage = 0xA1u;    // page number out of range
 constexpr uint32_t kSiteLen = 0xA2u;     // sequence length out of range
 constexpr uint32_t kSiteOffset = 0xA3u;  // packed offsets out of range or descending
-constexpr uint32_t kSiteSlot = 0xA4u;    // a new token without a slot
+constexpr uint32_t kSiteSlot = 0xA4u;    // a token without a slot
+constexpr uint32_t kSiteWeight = 0xA5u;  // a weight that is not finite
 
 // Cached tokens of sequence b, clamped to what its table row can hold.
 __device__ __forceinline__ int paged_len(const PagedView &c, int b, uint32_t *status) {
@@ -72,6 +74,20 @@ __device__ __forceinline__ int paged_page(const int32_t *table, int64_t stride, 
 // Element offset of slot t's row of KV head g inside page `page`.
 __device__ __forceinline__ int64_t paged_offset(const PagedView &c, int page, int t, int g) {
   return page * c.page_stride + (static_cast<int64_t>(t & ((1 << c.page_shift) - 1)) * c.Hkv + g) * c.d;
+}
+
+// Allows a kernel `bytes` of dynamic shared memory, once per device.
+template <auto Kernel>
+spts_status allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done[4];
+  int dev = 0;
+  SPTS_CUDA_TRY(cudaGetDevice(&dev));
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  std::atomic<uint64_t> &word = done[(dev >> 6) & 3];
+  if (dev < 256 && (word.load(std::memory_order_acquire) & bit)) return SPTS_OK;
+  SPTS_CUDA_TRY(cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)));
+  word.fetch_or(bit, std::memory_order_release);
+  return SPTS_OK;
 }
 
 // Launches a kernel that may start while the one before it on the stream still

@@ -865,8 +865,7 @@ constexpr int GROUPS = 1;
 template <int D, bool EXACT>
 spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, int ctas,
                    cudaStream_t s) {
-  SPTS_CUDA_TRY(cudaFuncSetAttribute(paged_attn_kernel<D, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem_bytes<D>())));
+  SPTS_TRY((allow_smem<paged_attn_kernel<D, EXACT>>(smem_bytes<D>())));
   paged_attn_kernel<D, EXACT><<<ctas, THREADS, smem_bytes<D>(), s>>>(tq, tk, tv, p);
   note_launch();
   SPTS_CUDA_TRY(cudaGetLastError());

@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(256) paged_weights_sum_kernel(PagedView c, con
 template <int D>
 spts_status launch(const CUtensorMap &q, const CUtensorMap &k, const Params &p, cudaStream_t s) {
   constexpr int bytes = 6 * (D / 64) * CHUNK + static_cast<int>(sizeof(Tail));
-  SPTS_CUDA_TRY(cudaFuncSetAttribute(paged_weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  SPTS_TRY((allow_smem<paged_weights_kernel<D>>(bytes)));
   paged_weights_kernel<D><<<num_sms(), THREADS, bytes, s>>>(q, k, p);
   note_launch();
   SPTS_CUDA_TRY(cudaGetLastError());
