@@ -144,6 +144,37 @@ __device__ __forceinline__ void store_8(float *to, const float *v) {
                : "memory");
 }
 
+// TMEM in rows of 16: thread t of the warp has row t / 4 (and t / 4 + 8) and,
+// of every 8 fp32 columns, columns 2 (t % 4) and the next.  ld: 8 N columns, 4 N
+// values {row, row, row + 8, row + 8}; st: 4 N columns of bf16 pairs, 2 N values
+// {row, row + 8}, so the pair a thread has loaded goes to the column it is at.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t addr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_rows16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 __device__ __forceinline__ int heads_of(const Params &p, int group) {
   return min(p.group_heads, p.c.Hkv - group * p.group_heads);
 }
@@ -521,6 +552,22 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t s_col = x * BKV;
     const float c2 = p.scale_log2;
+    // this row's O_x by `factor`
+    auto rescale_o = [&](float factor) {
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(lane_base + 256 + x * 128 + c * 32, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+        tmem_st32(lane_base + 256 + x * 128 + c * 32, o);
+      }
+      tmem_st_wait();
+    };
+    // For units of at most 16 rows: thread t has rows t / 4 and t / 4 + 8 of
+    // every tile, a quarter of their columns each.
+    const int na = (lane >> 2) / p.G, nb = ((lane >> 2) + 8) / p.G;  // their tokens
     uint32_t used = 0, joins = 0;  // tiles processed, exchanges with the other warpgroup
     bool ok = true;
     for (int item = 0; ok; ++item) {
@@ -550,9 +597,110 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       const bool any_live = __any_sync(0xffffffffu, live);
+      const bool few = !two && (it->n - it->tok0) * p.G <= 16;
       float m_run = -INFINITY, l = 0.f;
       int j0 = (t0 + (step == 2 ? x : 0)) * BKV;
-      for (int i = 0; i < own_tiles; ++i, j0 += step * BKV) {
+      if (few && quad == 0) {
+        // At most 16 rows: with a thread per row a warp would walk 128 columns
+        // with most of its lanes idle, and the key tile would wait for it (one
+        // row over 128K slots: TODO us, against 103.6).
+        const PlanSeq s{it->n, it->L};
+        const int tok0 = it->tok0, left = s.n - tok0;
+        const int lim_a = na < left ? plan_visible(s, tok0 + na + 1) : 0;
+        const int lim_b = nb < left ? plan_visible(s, tok0 + nb + 1) : 0;
+        float m2[2] = {-INFINITY, -INFINITY}, l2[2] = {0.f, 0.f};
+        const int my = 2 * (lane & 3);
+        for (int i = 0; i < own_tiles; ++i, j0 += 2 * BKV) {
+          const uint32_t u = used + i;
+          ok = __all_sync(0xffffffffu, mbar_wait(&t.s_full[x], u & 1, abort_flag, p.status, p.wait_ns, 0x5Bu));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t xr[64];
+          tmem_ld_rows16(lane_base + s_col, xr);
+          tmem_ld_wait();
+          if (j0 + BKV > mask_from) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+              const int col = (e >> 2) * 8 + my + (e & 1);
+              if (col >= ((e & 2) ? lim_b : lim_a) - j0) xr[e] = 0xff800000u;  // -inf
+            }
+          }
+          float f2[2];
+          bool need = false;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float a = __uint_as_float(xr[2 * h]), b = __uint_as_float(xr[2 * h + 1]);
+#pragma unroll
+            for (int e = 4; e < 64; e += 8) {
+              a = max3_nan(a, __uint_as_float(xr[e + 2 * h]), __uint_as_float(xr[e + 2 * h + 1]));
+              if (e + 4 < 64) b = max3_nan(b, __uint_as_float(xr[e + 4 + 2 * h]), __uint_as_float(xr[e + 5 + 2 * h]));
+            }
+            float top = max_nan(a, b);
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2)) * c2;
+            const float m_new = max_nan(m2[h], top);
+            f2[h] = 1.f;
+            if ((h ? lim_b : lim_a) > 0 && !(m_new <= m2[h] + RESCALE_THRESHOLD)) {
+              need = true;
+              f2[h] = m2[h] == -INFINITY ? 0.f : ex2(m2[h] - m_new);
+              m2[h] = m_new;
+              l2[h] *= f2[h];
+            }
+          }
+          if (__any_sync(0xffffffffu, need) && i > 0) {
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait(&t.o_done[x], (u - 1) & 1, abort_flag, p.status, p.wait_ns, 0x5Cu));
+            if (!ok) break;
+            tc_fence_after();
+            const float fa = __shfl_sync(0xffffffffu, f2[0], (lane & 7) * 4);
+            const float fb = __shfl_sync(0xffffffffu, f2[1], (lane & 7) * 4);
+            rescale_o(lane < 8 ? fa : fb);
+          }
+          const uint64_t cc = f2pack(c2, c2);
+          uint64_t mm[2], s2[2] = {0ull, 0ull};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float neg = m2[h] == -INFINITY ? 0.f : -m2[h];
+            mm[h] = f2pack(neg, neg);
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int h = e & 1, at = (half * 8 + (e >> 1)) * 4 + 2 * h;
+              float a0, a1;
+              f2unpack(f2fma(f2pack(__uint_as_float(xr[at]), __uint_as_float(xr[at + 1])), cc, mm[h]), a0, a1);
+              a0 = ex2(a0);
+              a1 = ex2(a1);
+              s2[h] = f2add(s2[h], f2pack(a0, a1));
+              pk[e] = pack_bf16x2(a0, a1);
+            }
+            tmem_st_rows16(lane_base + s_col + half * 32, pk);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&t.p_ready[2 * x + half]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float a, b;
+            f2unpack(s2[h], a, b);
+            l2[h] += a + b;
+          }
+        }
+        // back to a thread per row
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          l2[h] += __shfl_xor_sync(0xffffffffu, l2[h], 1);
+          l2[h] += __shfl_xor_sync(0xffffffffu, l2[h], 2);
+          const float mr = __shfl_sync(0xffffffffu, m2[h], (lane & 7) * 4);
+          const float lr = __shfl_sync(0xffffffffu, l2[h], (lane & 7) * 4);
+          if ((lane >> 3) == h) {
+            m_run = mr;
+            l = lr;
+          }
+        }
+      } else for (int i = 0; i < own_tiles; ++i, j0 += step * BKV) {
         const uint32_t u = used + i;
         ok = __all_sync(0xffffffffu, mbar_wait(&t.s_full[x], u & 1, abort_flag, p.status, p.wait_ns, 0x5Bu));
         if (!ok) break;
@@ -591,16 +739,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             mbar_wait(&t.o_done[x], (u - 1) & 1, abort_flag, p.status, p.wait_ns, 0x5Cu));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(lane_base + 256 + x * 128 + c * 32, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
-              tmem_st32(lane_base + 256 + x * 128 + c * 32, o);
-            }
-            tmem_st_wait();
+            rescale_o(factor);
           }
           l *= factor;
           m_run = m_new;
