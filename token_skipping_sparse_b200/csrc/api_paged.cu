@@ -70,6 +70,10 @@ size_t weights_scratch(const spts_attn_desc *a, const spts_paged_cache *c) {
   return paged_weights_scratch(c->B, static_cast<int64_t>(c->max_pages) * c->page_size, a->Hkv, 1);
 }
 
+size_t scores_bytes(const spts_attn_desc *a, const spts_paged_cache *c, int64_t T) {
+  return paged_scores_bytes(c->B, T, static_cast<int64_t>(c->max_pages) * c->page_size, a->Hq, a->Hkv);
+}
+
 }  // namespace
 
 extern "C" {
@@ -98,11 +102,12 @@ spts_status spts_cache_append(const spts_attn_desc *a, const spts_paged_cache *c
 size_t spts_paged_attention_workspace(const spts_attn_desc *a, const spts_paged_cache *c, int64_t T,
                                       int with_weights) {
   size_t b = kStatusBytes;
-  if (a == nullptr || c == nullptr || T <= 0 || a->Hq <= 0) return b;
+  if (a == nullptr || c == nullptr || T <= 0 || a->Hq <= 0 || a->Hkv <= 0 || c->B <= 0) return b;
   b += Carver::round(paged_attn_scratch_bytes(a->d));
   if (with_weights) {
     b += Carver::round(static_cast<size_t>(T) * a->Hq * sizeof(float));  // lse
-    b += Carver::round(weights_scratch(a, c) * sizeof(float));
+    const size_t scores = scores_bytes(a, c, T);
+    b += Carver::round(scores ? scores : weights_scratch(a, c) * sizeof(float));
   }
   return b;
 }
@@ -132,12 +137,14 @@ spts_status spts_paged_attention(const spts_attn_desc *a, const spts_paged_cache
   if (T == 0) return SPTS_OK;
   Carver cv(ws, ws_bytes);
   PagedAttnArgs args{q, q_stride, cu_q, T, a->Hq, 0.f, o, o_stride, lse, weights, weights ? Hs : 1, w_stride,
-                     cv.status(), cv.take(paged_attn_scratch_bytes(a->d)), nullptr};
+                     cv.status(), cv.take(paged_attn_scratch_bytes(a->d)), nullptr, nullptr};
   args.scale = a->scale > 0.f ? a->scale : 1.0f / std::sqrt(static_cast<float>(a->d));
   if (weights) {
     float *own = static_cast<float *>(cv.take(static_cast<size_t>(T) * a->Hq * sizeof(float)));
     if (lse == nullptr) args.lse = own;
-    args.w_scratch = static_cast<float *>(cv.take(weights_scratch(a, c) * sizeof(float)));
+    const size_t scores = scores_bytes(a, c, T);
+    float *rest = static_cast<float *>(cv.take(scores ? scores : weights_scratch(a, c) * sizeof(float)));
+    (scores ? args.scores : args.w_scratch) = rest;
   }
   return launch_paged_attention(view, args, cs(stream));
 }

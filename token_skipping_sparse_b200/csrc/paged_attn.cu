@@ -116,6 +116,8 @@ struct Params {
   float *part_o;    // [groups][ctas][2][SLOT_ROWS][D]
   float2 *part_ml;  // [groups][ctas][2][SLOT_ROWS]: running maximum (log2) and sum
   PlanCut *cuts;    // [groups][ctas]
+  float *scores;    // [T, Hq, score_stride] or NULL: q . k of every row and slot, for the weights
+  int64_t score_stride;
   uint32_t *status;
   uint64_t wait_ns;
 };
@@ -264,7 +266,7 @@ __device__ __forceinline__ void read_sequences(Tail &t, const Params &p) {
   __syncthreads();
 }
 
-template <int D, bool EXACT>
+template <int D, bool EXACT, bool FEW>
 __global__ void __launch_bounds__(THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       const bool any_live = __any_sync(0xffffffffu, live);
-      const bool few = !two && (it->n - it->tok0) * p.G <= 16;
+      const bool few = FEW && !two && (it->n - it->tok0) * p.G <= 16;
       float m_run = -INFINITY, l = 0.f;
       int j0 = (t0 + (step == 2 ? x : 0)) * BKV;
       if (few && quad == 0) {
@@ -618,6 +620,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           uint32_t xr[64];
           tmem_ld_rows16(lane_base + s_col, xr);
           tmem_ld_wait();
+          if (EXACT && p.scores) {
+            // the rows' scores as they are: a slot past a row's limit is not read again
+            const int64_t row = (static_cast<int64_t>(it->first + tok0) * p.Hq + it->g * p.G) * p.score_stride + j0 + my;
+            const int64_t row_a = row + (static_cast<int64_t>(na) * p.Hq + (lane >> 2) - na * p.G) * p.score_stride;
+            const int64_t row_b = row + (static_cast<int64_t>(nb) * p.Hq + (lane >> 2) + 8 - nb * p.G) * p.score_stride;
+#pragma unroll
+            for (int e = 0; e < 64; e += 2)
+              if ((e & 2) ? nb < left : na < left)
+                *reinterpret_cast<uint2 *>(p.scores + ((e & 2) ? row_b : row_a) + (e >> 2) * 8) =
+                    make_uint2(xr[e], xr[e + 1]);
+          }
           if (j0 + BKV > mask_from) {
 #pragma unroll
             for (int e = 0; e < 64; ++e) {
@@ -716,6 +729,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int c = 0; c < 4; ++c)
           tmem_ld32(lane_base + s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(xr + 32 * c));
         tmem_ld_wait();
+        if (FEW && EXACT && p.scores && live) {
+          uint4 *to = reinterpret_cast<uint4 *>(
+              p.scores + (static_cast<int64_t>(it->first + it->tok0 + (two ? x * p.tq : 0) + rt) * p.Hq + it->g * p.G + rh) *
+                             p.score_stride + j0);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) to[e] = make_uint4(xr[4 * e], xr[4 * e + 1], xr[4 * e + 2], xr[4 * e + 3]);
+        }
         if (j0 + BKV > mask_from) {  // slots past the tile's first query, past the last slot among them
           const int vis = lim - j0;
 #pragma unroll
@@ -912,6 +932,7 @@ template <int D>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __grid_constant__ Params p, int ctas) {
   const int range = blockIdx.x + 1, group = blockIdx.y;
   constexpr int E = D / 32;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PlanCut cut = p.cuts[group * ctas + range];
   if (!plan_first_cut(cut, range)) return;
@@ -1001,11 +1022,11 @@ Scratch carve(void *base, int d, int groups, int ctas) {
 
 constexpr int GROUPS = 1;
 
-template <int D, bool EXACT>
+template <int D, bool EXACT, bool FEW>
 spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, int ctas,
                    cudaStream_t s) {
-  SPTS_TRY((allow_smem<paged_attn_kernel<D, EXACT>>(smem_bytes<D>())));
-  paged_attn_kernel<D, EXACT><<<ctas, THREADS, smem_bytes<D>(), s>>>(tq, tk, tv, p);
+  SPTS_TRY((allow_smem<paged_attn_kernel<D, EXACT, FEW>>(smem_bytes<D>())));
+  paged_attn_kernel<D, EXACT, FEW><<<ctas, THREADS, smem_bytes<D>(), s>>>(tq, tk, tv, p);
   note_launch();
   SPTS_CUDA_TRY(cudaGetLastError());
   if (ctas > 1) {
@@ -1028,6 +1049,21 @@ spts_status paged_maps(const PagedView &c, const PagedAttnArgs &a, CUtensorMap *
   const uint32_t box[4] = {64, 1, static_cast<uint32_t>(page < PLAN_TILE ? page : PLAN_TILE), 1};
   SPTS_TRY(make_tmap(k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B));
   return make_tmap(v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Whether the sequences have 16 rows of a KV head or less on average: then
+// the kernel with the extra path for such units.  (Without it the full
+// units' loop is a little faster: an 8K prompt 480 us against 499.)
+static bool few_rows(int B, int64_t T, int G) { return T * G <= 16 * static_cast<int64_t>(B); }
+static int64_t score_stride(int64_t slots) { return (slots + BKV - 1) / BKV * BKV; }
+
+// With few rows the attention leaves its scores (G fp32 values per slot and
+// KV head, against d bf16 values of K for computing them again), as long as
+// they stay below SCORE_BYTES.
+constexpr size_t SCORE_BYTES = size_t(256) << 20;
+size_t paged_scores_bytes(int B, int64_t T, int64_t slots, int Hq, int Hkv) {
+  const size_t bytes = static_cast<size_t>(T) * Hq * score_stride(slots) * sizeof(float);
+  return few_rows(B, T, Hq / Hkv) && bytes <= SCORE_BYTES ? bytes : 0;
 }
 
 size_t paged_attn_scratch_bytes(int d) { return carve(nullptr, d, GROUPS, num_sms()).bytes; }
@@ -1056,11 +1092,15 @@ spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, c
   p.cuts = sc.cuts;
   p.status = a.status;
   p.wait_ns = wait_limit_ns();
-  const bool exact = a.lse != nullptr;
-  if (D == 64)
-    SPTS_TRY((exact ? launch<64, true> : launch<64, false>)(tq_map, tk_map, tv_map, p, ctas, s));
-  else
-    SPTS_TRY((exact ? launch<128, true> : launch<128, false>)(tq_map, tk_map, tv_map, p, ctas, s));
+  const bool exact = a.lse != nullptr, few = few_rows(c.B, a.T, G);
+  p.scores = a.weights && a.scores ? a.scores : nullptr;
+  p.score_stride = score_stride(static_cast<int64_t>(c.max_pages) << c.page_shift);
+  auto run = D == 64 ? (exact ? (few ? launch<64, true, true> : launch<64, true, false>)
+                              : (few ? launch<64, false, true> : launch<64, false, false>))
+                     : (exact ? (few ? launch<128, true, true> : launch<128, true, false>)
+                              : (few ? launch<128, false, true> : launch<128, false, false>));
+  SPTS_TRY(run(tq_map, tk_map, tv_map, p, ctas, s));
+  if (p.scores) return launch_stored_weights(c, a, p.score_stride, s);
   return a.weights ? launch_paged_weights(c, a, tq_map, tk_map, s) : SPTS_OK;
 }
 

@@ -351,6 +351,40 @@ __global__ void __launch_bounds__(256) paged_weights_sum_kernel(PagedView c, con
   }
 }
 
+// The same from the scores that the attention left (few rows): a thread has
+// four slots and walks the rows that see them.  Bound by reading the scores
+// and the weights.
+__global__ void __launch_bounds__(128) stored_weights_kernel(PagedView c, const int32_t *__restrict__ cu, int T, int Hq,
+                                                             float scale_log2, const float *scores,
+                                                             int64_t score_stride, const float *lse, float *weights,
+                                                             int Hs, int64_t w_stride, int chunks) {
+  const int unit = blockIdx.x / chunks, chunk = blockIdx.x % chunks, b = unit / Hs, hs = unit % Hs;
+  int first, n;
+  packed_span(cu, T, b, nullptr, first, n);
+  const int L = paged_len(c, b, nullptr), slot = (chunk * 128 + threadIdx.x) * 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (slot >= L || n == 0) return;
+  const int heads = Hq / Hs, base = L - n;
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = max(slot - base, 0); i < n; ++i) {
+    const int64_t row = static_cast<int64_t>(first + i) * Hq + hs * heads;
+    const int seen = base + i - slot;  // slots 0..seen of the four
+#pragma unroll 4
+    for (int h = 0; h < heads; ++h) {
+      const float4 s = *reinterpret_cast<const float4 *>(scores + (row + h) * score_stride + slot);
+      const float l = -LOG2E * lse[row + h];
+      sum[0] += ex2(fmaf(s.x, scale_log2, l));
+      if (seen >= 1) sum[1] += ex2(fmaf(s.y, scale_log2, l));
+      if (seen >= 2) sum[2] += ex2(fmaf(s.z, scale_log2, l));
+      if (seen >= 3) sum[3] += ex2(fmaf(s.w, scale_log2, l));
+    }
+  }
+  float *w = weights + (static_cast<int64_t>(b) * Hs + hs) * w_stride + slot;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (slot + e < L) w[e] += sum[e];
+}
+
 template <int D>
 spts_status launch(const CUtensorMap &q, const CUtensorMap &k, const Params &p, cudaStream_t s) {
   constexpr int bytes = 6 * (D / 64) * CHUNK + static_cast<int>(sizeof(Tail));
@@ -362,6 +396,13 @@ spts_status launch(const CUtensorMap &q, const CUtensorMap &k, const Params &p, 
 }
 
 }  // namespace
+
+spts_status launch_stored_weights(const PagedView &c, const PagedAttnArgs &a, int64_t score_stride, cudaStream_t s) {
+  const int64_t slots = static_cast<int64_t>(c.max_pages) << c.page_shift, chunks = (slots + 511) / 512;
+  return launch_behind(stored_weights_kernel, dim3(static_cast<unsigned>(chunks * c.B * a.Hs)), 128, s, c, a.cu,
+                       static_cast<int>(a.T), a.Hq, a.scale * LOG2E, static_cast<const float *>(a.scores), score_stride,
+                       static_cast<const float *>(a.lse), a.weights, a.Hs, a.w_stride, static_cast<int>(chunks));
+}
 
 size_t paged_weights_scratch(int B, int64_t slots, int Hkv, int Hs) {
   const size_t n = static_cast<size_t>(B) * Hkv * slots;
