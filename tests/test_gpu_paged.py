@@ -189,6 +189,34 @@ def test_attention_flat_and_sharp_scores(gain):
     assert np.all(np.abs(f64(e) - want["lse"]) <= err + 2.0 ** -21 * (1 + np.abs(want["lse"])))
 
 
+@pytest.mark.parametrize("each", [True, False])
+def test_attention_long_enough_for_head_groups(each):
+    # K and V of 82 MB shared by 19 windows of new tokens: the heads are taken in groups.  fp64 on the GPU, head by head
+    n, L, Hq, Hkv, d, page = 1201, 20003, 32, 8, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(41)
+    n_pages = -(-L // page)
+    k, v = (torch.randn(n_pages, page, Hkv, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    k.view(-1, Hkv, d)[L:], v.view(-1, Hkv, d)[L:] = float("nan"), float("nan")
+    q = (torch.randn(n, Hq, d, generator=g, device="cuda") * 2).bfloat16()
+    table = torch.arange(n_pages, dtype=I32, device="cuda")[None]
+    w = torch.zeros(1, Hkv if each else 1, n_pages * page, device="cuda")
+    o, e = S.spts_paged_attention(q, k, v, table, i32([L]), i32([0, n]), lse=True, weights=w)
+    S.check_device_status()
+    sees = torch.arange(L, device="cuda") <= L - n + torch.arange(n, device="cuda")[:, None]
+    want_w = torch.zeros(w.shape, dtype=torch.float64, device="cuda")
+    for h in range(Hq):
+        K, V = (x.view(-1, Hkv, d)[:L, h // (Hq // Hkv)].double() for x in (k, v))
+        s = (q[:, h].double() @ K.T * d ** -0.5).masked_fill(~sees, -np.inf)
+        err = (d + 4) * 2.0 ** -23 * float((q[:, h].double().abs() @ K.abs().T).max()) * d ** -0.5
+        a = s.softmax(-1)
+        bound = (U + 2 * err + 2.5e-4) * (a @ V.abs()) + U * (a @ V).abs()
+        assert bool(((o[:, h].double() - a @ V).abs() <= bound).all()), h
+        assert bool(((e[:, h].double() - s.logsumexp(-1)).abs() <= err + 2.0 ** -21 * (1 + s.logsumexp(-1).abs())).all())
+        want_w[0, h // (Hq // Hkv) if each else 0, :L] += a.sum(0)
+    bound = (2 * err + 2.0 ** -19 + n * (Hq // w.shape[1]) * 2.0 ** -24) * want_w
+    assert bool(((w.double() - want_w).abs() <= bound).all())
+
+
 def test_one_sequence_does_not_reach_another():
     # non-finite rows of one sequence, and of its neighbour in the packed rows
     c = Cache([100, 50, 70], 16, 2, 128, seed=17)

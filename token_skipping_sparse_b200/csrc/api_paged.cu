@@ -70,6 +70,10 @@ size_t weights_scratch(const spts_attn_desc *a, const spts_paged_cache *c) {
   return paged_weights_scratch(c->B, static_cast<int64_t>(c->max_pages) * c->page_size, a->Hkv, 1);
 }
 
+size_t attn_scratch(const spts_attn_desc *a, const spts_paged_cache *c, int64_t T) {
+  return paged_attn_scratch_bytes(c->B, T, static_cast<int64_t>(c->max_pages) * c->page_size, a->Hq, a->Hkv, a->d);
+}
+
 size_t scores_bytes(const spts_attn_desc *a, const spts_paged_cache *c, int64_t T) {
   return paged_scores_bytes(c->B, T, static_cast<int64_t>(c->max_pages) * c->page_size, a->Hq, a->Hkv);
 }
@@ -102,8 +106,10 @@ spts_status spts_cache_append(const spts_attn_desc *a, const spts_paged_cache *c
 size_t spts_paged_attention_workspace(const spts_attn_desc *a, const spts_paged_cache *c, int64_t T,
                                       int with_weights) {
   size_t b = kStatusBytes;
-  if (a == nullptr || c == nullptr || T <= 0 || a->Hq <= 0 || a->Hkv <= 0 || c->B <= 0) return b;
-  b += Carver::round(paged_attn_scratch_bytes(a->d));
+  if (a == nullptr || c == nullptr || T <= 0 || a->Hkv <= 0 || a->Hq < a->Hkv || a->Hq / a->Hkv > 128 || c->B <= 0 ||
+      c->max_pages <= 0 || c->page_size <= 0)
+    return b;
+  b += Carver::round(attn_scratch(a, c, T));
   if (with_weights) {
     b += Carver::round(static_cast<size_t>(T) * a->Hq * sizeof(float));  // lse
     const size_t scores = scores_bytes(a, c, T);
@@ -137,7 +143,7 @@ spts_status spts_paged_attention(const spts_attn_desc *a, const spts_paged_cache
   if (T == 0) return SPTS_OK;
   Carver cv(ws, ws_bytes);
   PagedAttnArgs args{q, q_stride, cu_q, T, a->Hq, 0.f, o, o_stride, lse, weights, weights ? Hs : 1, w_stride,
-                     cv.status(), cv.take(paged_attn_scratch_bytes(a->d)), nullptr, nullptr};
+                     cv.status(), cv.take(attn_scratch(a, c, T)), nullptr, nullptr};
   args.scale = a->scale > 0.f ? a->scale : 1.0f / std::sqrt(static_cast<float>(a->d));
   if (weights) {
     float *own = static_cast<float *>(cv.take(static_cast<size_t>(T) * a->Hq * sizeof(float)));

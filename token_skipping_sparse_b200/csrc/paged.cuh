@@ -126,14 +126,14 @@ struct PagedAttnArgs {
   int Hs;
   int64_t w_stride;
   uint32_t *status;
-  void *scratch;     // paged_attn_scratch_bytes(d)
+  void *scratch;     // paged_attn_scratch_bytes(...)
   float *w_scratch;  // paged_weights_scratch(...) floats, or NULL
   float *scores;     // paged_scores_bytes(...), or NULL
 };
 // TMA maps of q (box: 64 columns x G heads x 128 / G tokens) and of the pages
 // (64 columns x one head x the rows of a page, at most 128).
 spts_status paged_maps(const PagedView &c, const PagedAttnArgs &a, CUtensorMap *q, CUtensorMap *k, CUtensorMap *v);
-size_t paged_attn_scratch_bytes(int d);
+size_t paged_attn_scratch_bytes(int B, int64_t T, int64_t slots, int Hq, int Hkv, int d);
 spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, cudaStream_t s);
 size_t paged_scores_bytes(int B, int64_t T, int64_t slots, int Hq, int Hkv);
 // Adds to a.weights what the attention that left a.lse gave each slot: from

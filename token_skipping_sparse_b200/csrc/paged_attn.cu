@@ -97,6 +97,7 @@ struct Tail {  // shared memory behind the tiles
   Item item[ITEMS];
   uint32_t tmem;
   int abort_flag;
+  int groups, group_heads;  // KV heads are taken in `groups` groups of at most group_heads
 };
 
 template <int D>
@@ -108,14 +109,14 @@ struct Params {
   PagedView c;
   const int32_t *cu;
   int T, Hq, G, tq;
-  int groups, group_heads;  // KV heads are taken in `groups` groups of at most group_heads
+  int max_groups;   // head groups that the scratch has room for
   float scale_log2;
   __nv_bfloat16 *o;
   int64_t o_stride;
   float *lse;
-  float *part_o;    // [groups][ctas][2][SLOT_ROWS][D]
-  float2 *part_ml;  // [groups][ctas][2][SLOT_ROWS]: running maximum (log2) and sum
-  PlanCut *cuts;    // [groups][ctas]
+  float *part_o;    // [max_groups][ctas][2][SLOT_ROWS][D]
+  float2 *part_ml;  // [max_groups][ctas][2][SLOT_ROWS]: running maximum (log2) and sum
+  PlanCut *cuts;    // [max_groups][ctas]
   float *scores;    // [T, Hq, score_stride] or NULL: q . k of every row and slot, for the weights
   int64_t score_stride;
   uint32_t *status;
@@ -177,8 +178,8 @@ __device__ __forceinline__ void tmem_st_rows16(uint32_t addr, const uint32_t (&r
       : "memory");
 }
 
-__device__ __forceinline__ int heads_of(const Params &p, int group) {
-  return min(p.group_heads, p.c.Hkv - group * p.group_heads);
+__device__ __forceinline__ int heads_of(const Tail &t, const Params &p, int group) {
+  return min(t.group_heads, p.c.Hkv - group * t.group_heads);
 }
 
 // A value that all lanes hold, so that the compiler knows it too: loop counts
@@ -197,8 +198,8 @@ __device__ __forceinline__ void walk(Tail &t, const Params &p) {
     ok = mbar_wait_long(&t.item_empty[i], ((count / ITEMS) & 1) ^ 1, abort_flag, p.status, p.wait_ns, 0x50u);
     return &t.item[i];
   };
-  for (int group = 0; ok && group < p.groups; ++group) {
-    const int heads = heads_of(p, group);
+  for (int group = 0; ok && group < t.groups; ++group) {
+    const int heads = heads_of(t, p, group);
     const int64_t total = t.before[p.c.B] * heads;
     const int nr = plan_ranges(total, gridDim.x);
     if (r >= nr) continue;
@@ -217,7 +218,7 @@ __device__ __forceinline__ void walk(Tail &t, const Params &p) {
       it->L = s.L;
       it->first = t.first[pc.b];
       it->tok0 = pc.p * w;
-      it->g = group * p.group_heads + pc.g;
+      it->g = group * t.group_heads + pc.g;
       it->two = s.n - pc.p * w > p.tq;
       it->t0 = pc.t0;
       it->t1 = pc.t1;
@@ -247,10 +248,11 @@ __device__ __forceinline__ void read_sequences(Tail &t, const Params &p) {
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    int64_t run = 0;
+    int64_t run = 0, shared = 0;  // cost; slots of sequences with several windows
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
       const int b = b0 + lane;
       int64_t x = 0;
+      if (b < p.c.B && t.seq[b].n > 2 * p.tq) shared += t.seq[b].L;
       if (b < p.c.B) x = plan_cost(plan_base(t.seq[b], 2 * p.tq), plan_windows(t.seq[b].n, 2 * p.tq), 2 * p.tq);
       int64_t incl = x;
 #pragma unroll
@@ -261,7 +263,13 @@ __device__ __forceinline__ void read_sequences(Tail &t, const Params &p) {
       if (b < p.c.B) t.before[b] = run + incl - x;
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) t.before[p.c.B] = run;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) shared += __shfl_xor_sync(0xffffffffu, shared, o);
+    if (lane == 0) {
+      t.before[p.c.B] = run;
+      t.groups = plan_groups(shared * p.c.Hkv * p.c.d * 4, run * p.c.Hkv, gridDim.x, p.c.Hkv, p.max_groups);
+      t.group_heads = (p.c.Hkv + t.groups - 1) / t.groups;
+    }
   }
   __syncthreads();
 }
@@ -901,17 +909,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
   // what this CTA's ranges leave for the combine kernel
-  if (threadIdx.x < p.groups) {
-    const int heads = heads_of(p, threadIdx.x), rg = blockIdx.x;
+  if (threadIdx.x < p.max_groups) {
+    const int group = threadIdx.x, heads = group < t.groups ? heads_of(t, p, group) : 0, rg = blockIdx.x;
     PlanCut cut{};
-    cut.total = t.before[p.c.B] * heads;
+    cut.total = heads > 0 ? t.before[p.c.B] * heads : 0;
     const int nr = plan_ranges(cut.total, gridDim.x);
     if (rg < nr && cut.total > 0) {
       PlanCursor cur;
       plan_open(cur, t.seq, t.before, p.c.B, 2 * p.tq, heads, plan_cut(cut.total, nr, rg), 1);
-      cut = PlanCut{cut.total, nr, cur.b, cur.p, cur.g, cur.off, cur.c};
+      cut = PlanCut{cut.total, nr, cur.b, cur.p, group * t.group_heads + cur.g, cur.off, cur.c};
     }
-    p.cuts[threadIdx.x * gridDim.x + rg] = cut;
+    p.cuts[group * gridDim.x + rg] = cut;
   }
   __syncthreads();
   if (warp == 1) {
@@ -939,7 +947,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __
   int first, n;
   packed_span(p.cu, p.T, cut.b, nullptr, first, n);
   const PlanSeq s{n, paged_len(p.c, cut.b, nullptr)};
-  const int w = 2 * p.tq, tok0 = cut.p * w, g = group * p.group_heads + cut.g;
+  const int w = 2 * p.tq, tok0 = cut.p * w, g = cut.g;
   const int rows = min(w, n - tok0) * p.G;
   const int tiles = (plan_visible(s, tok0 + w) + BKV - 1) / BKV;
   const int lane = threadIdx.x & 31;
@@ -1020,7 +1028,6 @@ Scratch carve(void *base, int d, int groups, int ctas) {
   return s;
 }
 
-constexpr int GROUPS = 1;
 
 template <int D, bool EXACT, bool FEW>
 spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, int ctas,
@@ -1030,7 +1037,7 @@ spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   note_launch();
   SPTS_CUDA_TRY(cudaGetLastError());
   if (ctas > 1) {
-    SPTS_TRY(launch_behind(paged_combine_kernel<D>, dim3(ctas - 1, p.groups, JOIN_SPLIT), 32 * JOIN_WARPS, s, p, ctas));
+    SPTS_TRY(launch_behind(paged_combine_kernel<D>, dim3(ctas - 1, p.max_groups, JOIN_SPLIT), 32 * JOIN_WARPS, s, p, ctas));
   }
   return SPTS_OK;
 }
@@ -1066,14 +1073,28 @@ size_t paged_scores_bytes(int B, int64_t T, int64_t slots, int Hq, int Hkv) {
   return few_rows(B, T, Hq / Hkv) && bytes <= SCORE_BYTES ? bytes : 0;
 }
 
-size_t paged_attn_scratch_bytes(int d) { return carve(nullptr, d, GROUPS, num_sms()).bytes; }
+// Head groups that the sizes known on the host can call for (up to MAX_GROUPS:
+// 40 MB of scratch each).
+constexpr int MAX_GROUPS = 4;
+static int max_groups(int B, int64_t T, int64_t slots, int Hq, int Hkv, int d, int ctas) {
+  const int64_t w = 2 * (128 / (Hq / Hkv)), windows = T / w + B;
+  return plan_groups(static_cast<int64_t>(B) * slots * Hkv * d * 4, windows * (slots + PLAN_TWO) * Hkv, ctas, Hkv,
+                     MAX_GROUPS);
+}
+
+size_t paged_attn_scratch_bytes(int B, int64_t T, int64_t slots, int Hq, int Hkv, int d) {
+  const int ctas = num_sms();
+  return carve(nullptr, d, max_groups(B, T, slots, Hq, Hkv, d, ctas), ctas).bytes;
+}
 
 spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, cudaStream_t s) {
   if (a.T == 0) return SPTS_OK;
   const int D = c.d, G = a.Hq / c.Hkv, tq = 128 / G, ctas = num_sms();
+  const int64_t slots = static_cast<int64_t>(c.max_pages) << c.page_shift;
   CUtensorMap tq_map, tk_map, tv_map;
   SPTS_TRY(paged_maps(c, a, &tq_map, &tk_map, &tv_map));
-  const Scratch sc = carve(a.scratch, D, GROUPS, ctas);
+  const int groups = max_groups(c.B, a.T, slots, a.Hq, c.Hkv, D, ctas);
+  const Scratch sc = carve(a.scratch, D, groups, ctas);
   Params p{};
   p.c = c;
   p.cu = a.cu;
@@ -1081,8 +1102,7 @@ spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, c
   p.Hq = a.Hq;
   p.G = G;
   p.tq = tq;
-  p.groups = GROUPS;
-  p.group_heads = (c.Hkv + GROUPS - 1) / GROUPS;
+  p.max_groups = groups;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.o = static_cast<__nv_bfloat16 *>(a.o);
   p.o_stride = a.o_stride;
@@ -1094,7 +1114,7 @@ spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, c
   p.wait_ns = wait_limit_ns();
   const bool exact = a.lse != nullptr, few = few_rows(c.B, a.T, G);
   p.scores = a.weights && a.scores ? a.scores : nullptr;
-  p.score_stride = score_stride(static_cast<int64_t>(c.max_pages) << c.page_shift);
+  p.score_stride = score_stride(slots);
   auto run = D == 64 ? (exact ? (few ? launch<64, true, true> : launch<64, true, false>)
                               : (few ? launch<64, false, true> : launch<64, false, false>))
                      : (exact ? (few ? launch<128, true, true> : launch<128, true, false>)

@@ -169,11 +169,26 @@ SPTS_HD int plan_next(PlanCursor &cur, const PlanSeq *seq, int B, int w, int hea
   return 1;
 }
 
+// Head groups (a power of two, at most `most`).  With one group the CTAs stand
+// at places spread over all keys of all heads, so K and V that several units
+// share must stay in L2 as a whole (2048 rows over 32K slots, 134 MB: 1.73 GB
+// read from HBM with one group, 0.17 GB with four).  More groups mean more
+// cuts, worth PLAN_GROUP_TILES of each CTA's tiles or more.
+constexpr int64_t PLAN_GROUP_BYTES = int64_t(72) << 20;
+constexpr int PLAN_GROUP_TILES = 64;
+SPTS_HD int plan_groups(int64_t shared_bytes, int64_t total, int ctas, int heads, int most) {
+  int groups = 1;
+  while (2 * groups <= most && 2 * groups <= heads && shared_bytes > groups * PLAN_GROUP_BYTES &&
+         total / PLAN_TILE >= static_cast<int64_t>(2) * groups * ctas * PLAN_GROUP_TILES)
+    groups *= 2;
+  return groups;
+}
+
 // What the range r leaves for the combine kernel about its first position.
 struct PlanCut {
   int64_t total;  // cost of the group
   int nr;         // its ranges (0: this range is not one of them)
-  int b, p, g;    // the unit at the cut
+  int b, p, g;    // the unit at the cut (g: counted over all heads)
   int off, c;     // how far inside it the cut is (0: between two units), and the unit's cost
 };
 
