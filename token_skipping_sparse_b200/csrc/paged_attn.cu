@@ -34,6 +34,8 @@
 // P is rounded to bf16 for the product with V (half a step, 2^-9 of each
 // weight); S, the maxima, the sums and O stay in fp32.
 // All barrier waits are bounded (see sm100.cuh).
+#include <type_traits>
+
 #include "host.hpp"
 #include "paged.cuh"
 #include "paged_plan.hpp"
@@ -53,9 +55,11 @@ constexpr int SLOT_ROWS = 256;        // rows of a partial result: two Q tiles
 constexpr uint32_t TMEM_COLS = 512;   // S_0 [0,128), S_1 [128,256), O_0 from 256, O_1 from 384
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 constexpr float LN2 = 0.69314718055994530942f;
-// One column pair in POLY_EVERY takes its exp2 from the FMA pipe when the
-// row sums serve the bf16 output alone; with lse or weights asked for, all
-// come from the MUFU pipe (2 ulp against 1e-4).
+// One column pair in POLY_EVERY takes its exp2 from the FMA pipe (exp2_poly2,
+// 1e-4, far below P's bf16 step) when the row sums serve the bf16 output
+// alone.  Where lse or weights are wanted all are the MUFU pipe's: a finer
+// polynomial for two fifths of them cost more registers than it gave (250
+// rows over 32K slots: 141 us against 134).
 constexpr int POLY_EVERY = 3;
 
 template <int D>
@@ -296,8 +300,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&t.q_full[x], 1);
       mbar_init(&t.q_empty[x], 1);
       mbar_init(&t.s_full[x], 1);
-      mbar_init(&t.p_ready[2 * x], 128);
-      mbar_init(&t.p_ready[2 * x + 1], 128);
+      mbar_init(&t.p_ready[2 * x], 4);  // here and below: one arrival per warp
+      mbar_init(&t.p_ready[2 * x + 1], 4);
       mbar_init(&t.o_done[x], 1);
     }
     for (int s = 0; s < STAGES; ++s) {
@@ -307,8 +311,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&t.v_empty[s], 1);
       mbar_init(&t.v_raw[s], 1);
     }
-    mbar_init(&t.o_free, 256);
-    mbar_init(&t.x_full, 256);
+    mbar_init(&t.o_free, 8);
+    mbar_init(&t.x_full, 8);
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(&t.item_full[i], 1);
       mbar_init(&t.item_empty[i], 11);  // a lane of every other warp
@@ -700,7 +704,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_st_rows16(lane_base + s_col + half * 32, pk);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&t.p_ready[2 * x + half]);
+            mbar_arrive_warp(&t.p_ready[2 * x + half]);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -727,8 +731,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
         if (!any_live) {  // a warp of padding rows: P may be anything
           tc_fence_before();
-          mbar_arrive(&t.p_ready[2 * x]);
-          mbar_arrive(&t.p_ready[2 * x + 1]);
+          mbar_arrive_warp(&t.p_ready[2 * x]);
+          mbar_arrive_warp(&t.p_ready[2 * x + 1]);
           continue;
         }
         tc_fence_after();
@@ -798,7 +802,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (h == 0) {
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&t.p_ready[2 * x]);
+            mbar_arrive_warp(&t.p_ready[2 * x]);
           }
         }
         {
@@ -809,7 +813,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&t.p_ready[2 * x + 1]);
+        mbar_arrive_warp(&t.p_ready[2 * x + 1]);
       }
       if (!ok) break;
       used += own_tiles;
@@ -830,7 +834,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!two && any_tile) {
         t.xchg[joins & 1][x][r] = make_float2(m_run, l);
         tc_fence_before();
-        mbar_arrive(&t.x_full);
+        mbar_arrive_warp(&t.x_full);
         ok = __all_sync(0xffffffffu,
                         mbar_wait(&t.x_full, joins & 1, abort_flag, p.status, p.wait_ns, 0x5Eu));
         if (!ok) break;
@@ -904,7 +908,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (any_tile) {
         tc_fence_before();
-        mbar_arrive(&t.o_free);
+        mbar_arrive_warp(&t.o_free);
       }
     }
   }
@@ -934,12 +938,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 // attention still runs (its CTAs take the places of those that ended), and
 // waits for it.
 constexpr int JOIN_WARPS = 8;
-constexpr int JOIN_SPLIT = 8;  // CTAs per unit
 
 template <int D>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __grid_constant__ Params p, int ctas) {
   const int range = blockIdx.x + 1, group = blockIdx.y;
   constexpr int E = D / 32;
+  using Vec = std::conditional_t<D == 128, float4, float2>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PlanCut cut = p.cuts[group * ctas + range];
@@ -960,7 +964,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __
     plan_tiles(off, end, cut.c, tiles, t0, t1);
     return t0 < t1 ? ((static_cast<int64_t>(group) * ctas + rg) * 2 + slot) * SLOT_ROWS : -1;
   };
-  for (int row = blockIdx.z * JOIN_WARPS + (threadIdx.x >> 5); row < rows; row += JOIN_SPLIT * JOIN_WARPS) {
+  for (int row = blockIdx.z * JOIN_WARPS + (threadIdx.x >> 5); row < rows; row += static_cast<int>(gridDim.z) * JOIN_WARPS) {
     float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -983,14 +987,25 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] *= keep;
       // pieces of which this row sees nothing are skipped: their O may be anything
-      uint32_t live = __ballot_sync(0xffffffffu, at >= 0 && ml.x != -INFINITY);
-      while (live) {
-        const int i = __ffs(live) - 1;
-        live &= live - 1;
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float *o = p.part_o + (__shfl_sync(0xffffffffu, at, i) + row) * D + lane * E;
+      const uint32_t live = __ballot_sync(0xffffffffu, at >= 0 && ml.x != -INFINITY);
+      const int pieces = 32 - __clz(live);
+      for (int j = 0; j < pieces; j += 4) {  // four pieces' rows in flight together
+        Vec v[4];
+        float fj[4];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(o[e], fi, acc[e]);
+        for (int q = 0; q < 4; ++q) {
+          const int i = (j + q) & 31;
+          fj[q] = __shfl_sync(0xffffffffu, f, i);
+          const int64_t from = __shfl_sync(0xffffffffu, at, i);
+          const bool on = j + q < pieces && ((live >> i) & 1u);
+          if (!on) fj[q] = 0.f;
+          if (on) v[q] = *reinterpret_cast<const Vec *>(p.part_o + (from + row) * D + lane * E);
+          else v[q] = Vec{};
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(reinterpret_cast<const float *>(&v[q])[e], fj[q], acc[e]);
       }
     }
     const int tok = first + tok0 + row / p.G, head = g * p.G + row % p.G;
@@ -1037,7 +1052,9 @@ spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   note_launch();
   SPTS_CUDA_TRY(cudaGetLastError());
   if (ctas > 1) {
-    SPTS_TRY(launch_behind(paged_combine_kernel<D>, dim3(ctas - 1, p.max_groups, JOIN_SPLIT), 32 * JOIN_WARPS, s, p, ctas));
+    // CTAs per unit: two rows of the largest window for each warp
+    const int most = (p.T < 2 * p.tq ? p.T : 2 * p.tq) * p.G, split = FEW ? 1 : (most + 2 * JOIN_WARPS - 1) / (2 * JOIN_WARPS);
+    SPTS_TRY(launch_behind(paged_combine_kernel<D>, dim3(ctas - 1, p.max_groups, split), 32 * JOIN_WARPS, s, p, ctas));
   }
   return SPTS_OK;
 }

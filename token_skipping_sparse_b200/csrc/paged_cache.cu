@@ -119,6 +119,12 @@ __device__ __forceinline__ uint32_t weight_key(float f) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// Sum of v[0..w) (32 entries in shared memory), by a whole warp.
+__device__ __forceinline__ uint32_t sum_below(const uint32_t *v, int w) {
+  const int lane = threadIdx.x & 31;
+  return __reduce_add_sync(0xffffffffu, lane < w ? v[lane] : 0u);
+}
+
 __device__ __forceinline__ uint32_t ld_cluster(const uint32_t *p, uint32_t cta) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, cta)) : "memory");
@@ -180,9 +186,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(PagedView c, 
     }
     if (lane == 31) warp_gt[w] = incl;
     __syncthreads();
-    uint32_t before = 0;
-    for (int i = 0; i < w; ++i) before += warp_gt[i];
-    const uint32_t above = before + incl - c0 - c1;  // keys in higher bins
+    const uint32_t above = sum_below(warp_gt, w) + incl - c0 - c1;  // keys in higher bins
     if (above < rem && rem <= above + c0) {
       s_digit = top;
       s_rem = rem - above;
@@ -217,11 +221,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(PagedView c, 
     warp_eq[w] = eq;
   }
   __syncthreads();
-  uint32_t gt0 = 0, eq0 = 0;
-  for (int i = 0; i < w; ++i) {
-    gt0 += warp_gt[i];
-    eq0 += warp_eq[i];
-  }
+  uint32_t gt0 = sum_below(warp_gt, w), eq0 = sum_below(warp_eq, w);
   if (tid == SEL_THREADS - 1) {
     totals[0] = gt0 + gt;
     totals[1] = eq0 + eq;
@@ -261,7 +261,8 @@ __device__ __forceinline__ int64_t src_offset(const PagedView &c, const EvictArg
 }
 
 constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_ROWS = 4;  // rows of a thread, all in flight together
+constexpr int MOVE_ROWS = 4;    // rows of a thread that are in flight together
+constexpr int COPY_ROWS = 128;  // rows of a CTA
 
 // The weights of one row's kept tokens, then zeros; in place too: a tile of
 // TILE entries is read before it is written, kept[t] >= t and ascending, so a
@@ -288,10 +289,14 @@ __device__ __forceinline__ void move_weights(const EvictArgs &e, int row, int n)
   for (int64_t t = n + threadIdx.x; t < e.w_out_stride; t += MOVE_THREADS) out[t] = 0.f;
 }
 
-// To other pages: every row on its own.  A thread has one 16-byte column of
-// MOVE_ROWS rows of K and V.  `parts` CTAs for the rows of each (sequence, KV
-// head), and one more that moves the weights.
+// To other pages: every row on its own.  A CTA has COPY_ROWS rows of a
+// (sequence, KV head): a thread first looks up one row's places (slot, page,
+// destination: three dependent loads, once per row and not once per piece of
+// it), then the K and V rows go over in 16-byte pieces, MOVE_ROWS of each in
+// flight per thread.  `parts` CTAs for each head, and one more that moves the
+// weights.
 __global__ void __launch_bounds__(MOVE_THREADS) evict_copy_kernel(PagedView c, EvictArgs e, int parts) {
+  __shared__ int64_t from[COPY_ROWS], to[COPY_ROWS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int unit = blockIdx.x / (parts + 1), part = blockIdx.x % (parts + 1), b = unit / c.Hkv, g = unit % c.Hkv;
   const int n = min(paged_len(c, b, nullptr), e.keep);
@@ -300,30 +305,35 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_copy_kernel(PagedView c, E
     if (g < e.Hs) move_weights(e, b * e.Hs + g, n);
     return;
   }
-  const int vecs = c.d / 8, per = MOVE_THREADS / vecs, r = threadIdx.x / vecs, x = threadIdx.x % vecs;
-  const int32_t *kept = e.kept + (static_cast<int64_t>(b) * e.Hs + (e.Hs == 1 ? 0 : g)) * e.kept_stride;
-  const int base = part * per * MOVE_ROWS;
-  if (base >= n) return;
-  int64_t from[MOVE_ROWS], to[MOVE_ROWS];
-  uint4 k[MOVE_ROWS], v[MOVE_ROWS];
-#pragma unroll
-  for (int u = 0; u < MOVE_ROWS; ++u) {
-    const int t = base + u * per + r;
-    from[u] = t < n ? src_offset(c, e, b, kept[t], g) : -1;
-    to[u] = t < n ? dst_offset(c, e, b, t, g) : -1;
+  const int base = part * COPY_ROWS, rows = min(n - base, COPY_ROWS);
+  if (rows <= 0) return;
+  const int32_t *kept = e.kept + (static_cast<int64_t>(b) * e.Hs + (e.Hs == 1 ? 0 : g)) * e.kept_stride + base;
+  if (threadIdx.x < rows) {
+    const int64_t f = src_offset(c, e, b, kept[threadIdx.x], g), t = dst_offset(c, e, b, base + threadIdx.x, g);
+    from[threadIdx.x] = t < 0 ? -1 : f;
+    to[threadIdx.x] = t;
   }
+  __syncthreads();
+  const int vecs = c.d / 8, per = MOVE_THREADS / vecs, x = threadIdx.x % vecs;
+  for (int r0 = threadIdx.x / vecs; r0 < rows; r0 += per * MOVE_ROWS) {
+    uint4 k[MOVE_ROWS], v[MOVE_ROWS];
 #pragma unroll
-  for (int u = 0; u < MOVE_ROWS; ++u)
-    if (from[u] >= 0 && to[u] >= 0) {
-      k[u] = reinterpret_cast<const uint4 *>(c.k + from[u])[x];
-      v[u] = reinterpret_cast<const uint4 *>(c.v + from[u])[x];
+    for (int u = 0; u < MOVE_ROWS; ++u) {
+      const int r = r0 + u * per;
+      if (r < rows && from[r] >= 0) {
+        k[u] = reinterpret_cast<const uint4 *>(c.k + from[r])[x];
+        v[u] = reinterpret_cast<const uint4 *>(c.v + from[r])[x];
+      }
     }
 #pragma unroll
-  for (int u = 0; u < MOVE_ROWS; ++u)
-    if (from[u] >= 0 && to[u] >= 0) {
-      reinterpret_cast<uint4 *>(c.k + to[u])[x] = k[u];
-      reinterpret_cast<uint4 *>(c.v + to[u])[x] = v[u];
+    for (int u = 0; u < MOVE_ROWS; ++u) {
+      const int r = r0 + u * per;
+      if (r < rows && from[r] >= 0) {
+        reinterpret_cast<uint4 *>(c.k + to[r])[x] = k[u];
+        reinterpret_cast<uint4 *>(c.v + to[r])[x] = v[u];
+      }
     }
+  }
 }
 
 // In place: one CTA per (sequence, KV head), K or V and 64-byte slice of the
@@ -411,8 +421,7 @@ spts_status launch_cache_evict(const PagedView &c, const EvictArgs &e, cudaStrea
   const int64_t slots = static_cast<int64_t>(c.max_pages) << c.page_shift;
   const int64_t units = static_cast<int64_t>(c.B) * c.Hkv;
   const int64_t most = e.keep < slots ? e.keep : slots;
-  const int per = MOVE_THREADS / (c.d / 8) * MOVE_ROWS;
-  const int parts = static_cast<int>((most + per - 1) / per);
+  const int parts = static_cast<int>((most + COPY_ROWS - 1) / COPY_ROWS);
   SPTS_REQUIRE(units * (parts + 1) < (int64_t(1) << 31), SPTS_ERR_SHAPE,
                "spts_cache_evict: too many rows for one call (%lld heads of sequences, %lld slots)",
                static_cast<long long>(units), static_cast<long long>(most));

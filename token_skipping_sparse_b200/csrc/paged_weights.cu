@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&t.s_full[i], 1);
-      mbar_init(&t.s_free[i], 128);
-      mbar_init(&t.lse_full[i], 128);
+      mbar_init(&t.s_free[i], 4);  // one arrival per warp
+      mbar_init(&t.lse_full[i], 4);
     }
     mbar_init(&t.drain, 1);
     t.abort_flag = 0;
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int buf = qc & 1;
           const uint32_t ph = (qc >> 1) & 1;
           reinterpret_cast<float *>(t.lse[x][buf])[r] = next;
-          mbar_arrive(&t.lse_full[2 * x + buf]);
+          mbar_arrive_warp(&t.lse_full[2 * x + buf]);
           next = lse_of(q + 1);
           ok = __all_sync(0xffffffffu, mbar_wait(&t.lse_full[2 * x + buf], ph, abort_flag, p.status, p.wait_ns, 0x66u));
           if (!ok) break;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tmem_ld32(lane_base + buf * 128 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(xr + 32 * c));
           tmem_ld_wait();
           tc_fence_before();
-          mbar_arrive(&t.s_free[2 * x + buf]);
+          mbar_arrive_warp(&t.s_free[2 * x + buf]);
           // rows of this tile that see the slot: tokens >= slot - base, up to the last one
           const int lo = (slot - base - q * p.tq) * p.G, hi = min(p.tq, s.n - q * p.tq) * p.G;
           if (__any_sync(0xffffffffu, lo > 0) || hi < 128) {
@@ -309,11 +309,21 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const ulonglong2 l2 = ls[e];
-            float a0, a1, b0, b1;
-            f2unpack(f2fma(f2pack(__uint_as_float(xr[4 * e]), __uint_as_float(xr[4 * e + 1])), cc, l2.x), a0, a1);
-            f2unpack(f2fma(f2pack(__uint_as_float(xr[4 * e + 2]), __uint_as_float(xr[4 * e + 3])), cc, l2.y), b0, b1);
-            sum[(2 * e) & 3] = f2add(sum[(2 * e) & 3], f2pack(ex2(a0), ex2(a1)));
-            sum[(2 * e + 1) & 3] = f2add(sum[(2 * e + 1) & 3], f2pack(ex2(b0), ex2(b1)));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int pair = 2 * e + i;
+              const uint64_t a2 = f2fma(f2pack(__uint_as_float(xr[2 * pair]), __uint_as_float(xr[2 * pair + 1])), cc,
+                                        i ? l2.y : l2.x);
+              float a, b;
+              if (pair % 5 == 1 || pair % 5 == 3) {  // two fifths on the FMA pipe
+                exp2_fine2(a2, a, b);
+              } else {
+                f2unpack(a2, a, b);
+                a = ex2(a);
+                b = ex2(b);
+              }
+              sum[pair & 3] = f2add(sum[pair & 3], f2pack(a, b));
+            }
           }
         }
       }

@@ -60,6 +60,12 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t by
                "r"(bytes)
                : "memory");
 }
+// One arrival for a whole warp, after all its lanes got here: 32 arrivals on
+// one barrier are 32 atomics on one word.
+__device__ __forceinline__ void mbar_arrive_warp(uint64_t *bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -484,6 +490,29 @@ __device__ __forceinline__ void exp2_poly2(uint64_t x2, float &e0, float &e1) {
   uint64_t p = f2fma(f2pack(0.055009059607982635f, 0.055009059607982635f), f,
                      f2pack(0.2422109693288803f, 0.2422109693288803f));
   p = f2fma(p, f, f2pack(0.6932829022407532f, 0.6932829022407532f));
+  p = f2fma(p, f, f2pack(1.0f, 1.0f));
+  float p0, p1, y0, y1;
+  f2unpack(p, p0, p1);
+  f2unpack(y, y0, y1);
+  e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(y0) << 23));
+  e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(y1) << 23));
+}
+
+// The same with a degree-5 polynomial (relative error 2.6e-7, fp32 rounding
+// included; coefficients from exp2_poly_fit.py too), where the exponentials
+// serve an fp32 output.
+__device__ __forceinline__ void exp2_fine2(uint64_t x2, float &e0, float &e1) {
+  float a, b;
+  f2unpack(x2, a, b);
+  const uint64_t x = f2pack(fmaxf(a, -127.f), fmaxf(b, -127.f));
+  const uint64_t y = f2add(x, f2pack(12582912.f, 12582912.f));
+  const uint64_t j = f2add(y, f2pack(-12582912.f, -12582912.f));
+  const uint64_t f = f2fma(j, f2pack(-1.f, -1.f), x);
+  uint64_t p = f2fma(f2pack(0.0013381302123889327f, 0.0013381302123889327f), f,
+                     f2pack(0.00966636836528778f, 0.00966636836528778f));
+  p = f2fma(p, f, f2pack(0.055503811687231064f, 0.055503811687231064f));
+  p = f2fma(p, f, f2pack(0.2402234971523285f, 0.2402234971523285f));
+  p = f2fma(p, f, f2pack(0.6931471824645996f, 0.6931471824645996f));
   p = f2fma(p, f, f2pack(1.0f, 1.0f));
   float p0, p1, y0, y1;
   f2unpack(p, p0, p1);
