@@ -186,11 +186,6 @@ __device__ __forceinline__ int heads_of(const Tail &t, const Params &p, int grou
   return min(t.group_heads, p.c.Hkv - group * t.group_heads);
 }
 
-// A value that all lanes hold, so that the compiler knows it too: loop counts
-// and ring places then live in uniform registers, where the MMA descriptors
-// have to be (2048 rows over 32K slots: TODO).
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-
 // Warp 3, one lane: the pieces of this CTA's ranges, group after group.
 __device__ __forceinline__ void walk(Tail &t, const Params &p) {
   volatile int *abort_flag = &t.abort_flag;

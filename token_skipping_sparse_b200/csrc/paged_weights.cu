@@ -5,14 +5,18 @@
 // A second pass over K once the rows' lse are known: S is computed again,
 // transposed, S^T = K Q^T, so that a TMEM lane is a slot and its sum over the
 // rows stays inside one thread: no atomics, a fixed order, the same bits every
-// time.  A unit is 256 slots (two K tiles of 128, one per warpgroup) of one KV
-// head; it keeps its K tiles in shared memory while the Q tiles of the
-// sequence (128 / G tokens x G heads each) stream past both, so Q comes from
-// L2 once per 256 slots.  Bound by the exponentials (16384 per K and Q tile:
-// 1024 cycles of the MUFU pipe against 256 of the MMA) when there are many
-// rows, by reading K when there are few.  All exponentials are the MUFU
-// pipe's: the output is fp32.
-//   warp 0  TMA, warp 1  MMA, warps 4..7 and 8..11  slots of K tile 0 and 1
+// time.  A unit is up to four K tiles of 128 slots of one KV head, one for each
+// of four warpgroups; they stay in shared memory while the Q tiles of the
+// sequence (128 / G tokens x G heads each) stream past all four.  (With two K
+// tiles per Q tile the Q loads were what everything waited for: without any
+// exponential 250 rows over 32K slots still took 90 of 126 us.)  Bound by the
+// exponentials (16384 per K and Q tile: 1024 cycles of the MUFU pipe against
+// 512 of the MMA) when there are many rows, by reading K when there are few.
+// All exponentials are the MUFU pipe's: the output is fp32.
+//   warp 0  TMA, warp 1  MMA, warp 3  hands out the units, warps 4..19  four
+//   warpgroups, one per K tile
+// The K tiles of all sequences and heads, weighted with their Q tiles, are
+// shared out evenly; a CTA's share is cut into units at heads and fours.
 // With one weight row for all heads (Hs = 1) the units of a slot's KV heads
 // leave partial sums that a last kernel adds in order, as long as their scratch
 // stays below SPLIT_BYTES; beyond, a unit walks all its heads itself.
@@ -24,22 +28,37 @@
 namespace spts {
 namespace {
 
-constexpr int THREADS = 384;
-constexpr int REG_LOW = 88, REG_HIGH = 208;  // 88 + 2 x 208 = 3 x 168
+constexpr int THREADS = 640;
+constexpr int REG_LOW = 56, REG_HIGH = 104;  // 56 + 4 x 104 <= 5 x 96, the launch allocation
+constexpr int WG = 4;  // warpgroups, and K tiles of a unit
 constexpr int BKV = PLAN_TILE;
 constexpr int CHUNK = 128 * 64 * 2;
 constexpr int MAX_SEQ = 1024;
-constexpr uint32_t TMEM_COLS = 512;  // S of warpgroup x, buffer i: columns [256 x + 128 i, + 128)
+constexpr uint32_t TMEM_COLS = 512;  // S^T of warpgroup w: columns [128 w, 128 w + 128)
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr size_t SPLIT_BYTES = size_t(64) << 20;
 
+constexpr int ITEMS = 4;
+
+// A unit, as the warps need it.
+struct Unit {
+  int more;          // 0 behind the last
+  int b, n, L;       // the sequence, its new and cached tokens
+  int first;         // packed row of its first new token
+  int g0, slot0;     // first KV head, first slot
+  int tiles;         // K tiles
+  int q0, q1;        // Q tiles that see any of its slots
+};
+
 struct Tail {
-  int64_t before[MAX_SEQ + 1];  // units of the sequences before
+  int64_t before[MAX_SEQ + 1];  // cost of the sequences before: K tiles x heads x Q tiles
   PlanSeq seq[MAX_SEQ];
   int first[MAX_SEQ];
-  alignas(16) float2 lse[2][2][64];  // per warpgroup, by turns: -lse (log2) of the Q tile's rows, in pairs
-  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2];
-  uint64_t s_full[4], s_free[4], lse_full[4], drain;
+  alignas(16) float lse[WG][2][128];  // per warpgroup, by turns: -lse (log2) of the Q tile's rows
+  uint64_t q_full[2], q_empty[2], k_full[WG], k_empty[WG];
+  uint64_t s_full[WG], s_free[WG], lse_full[2 * WG], drain;
+  uint64_t item_full[ITEMS], item_empty[ITEMS];
+  Unit item[ITEMS];
   uint32_t tmem;
   int abort_flag;
 };
@@ -65,29 +84,63 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-struct Unit {
-  int b, g0, slot0;  // sequence, first KV head, first slot
-  int q0, q1;        // Q tiles that see any of its slots
-};
+__device__ __forceinline__ int k_tiles(int L) { return (L + BKV - 1) / BKV; }
+__device__ __forceinline__ int q_tiles(int n, int tq) { return (n + tq - 1) / tq; }
 
-// Unit u of the list (sequence, pair of K tiles, head).
-__device__ __forceinline__ Unit unit_at(const Tail &t, const Params &p, int64_t u) {
-  int lo = 0, hi = p.c.B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.before[mid] <= u) lo = mid;
-    else hi = mid - 1;
+// Warp 3, one lane: this CTA's units, handed to the other warps through a
+// ring.  K tiles are ordered by (sequence, head, slot); a tile belongs to the
+// CTA whose equal share of the cost its first position falls into.
+__device__ __forceinline__ void walk(Tail &t, const Params &p) {
+  volatile int *abort_flag = &t.abort_flag;
+  const int heads = p.c.Hkv / p.unit_heads;  // head by head, or all at once
+  const int64_t total = t.before[p.c.B];
+  const int64_t lo = plan_cut(total, gridDim.x, blockIdx.x), hi = plan_cut(total, gridDim.x, blockIdx.x + 1);
+  int count = 0;
+  auto place = [&]() -> Unit * {
+    const int i = count % ITEMS;
+    const bool ok =
+        mbar_wait_long(&t.item_empty[i], ((count / ITEMS) & 1) ^ 1, abort_flag, p.status, p.wait_ns, 0x60u);
+    return ok ? &t.item[i] : nullptr;
+  };
+  for (int b = 0; b < p.c.B && t.before[b] < hi; ++b) {
+    if (t.before[b + 1] <= lo) continue;
+    const PlanSeq s = t.seq[b];
+    const int tiles = k_tiles(s.L), cost = q_tiles(s.n, p.tq);
+    if (tiles == 0 || cost == 0) continue;
+    // tiles [from, to) of the sequence's tiles of all heads begin in this share
+    const int64_t all = static_cast<int64_t>(tiles) * heads;
+    const int64_t x = lo - t.before[b], y = hi - t.before[b];
+    const int64_t from = x <= 0 ? 0 : (x + cost - 1) / cost, to = y >= all * cost ? all : (y + cost - 1) / cost;
+    int g = static_cast<int>(from / tiles), j = static_cast<int>(from - static_cast<int64_t>(g) * tiles);
+    for (int64_t k = from; k < to;) {
+      const int64_t left = to - k;
+      const int take = min(min(WG, tiles - j), left < WG ? static_cast<int>(left) : WG);
+      Unit *r = place();
+      if (r == nullptr) return;
+      r->more = 1;
+      r->b = b;
+      r->n = s.n;
+      r->L = s.L;
+      r->first = t.first[b];
+      r->g0 = g * p.unit_heads;
+      r->slot0 = j * BKV;
+      r->tiles = take;
+      r->q0 = max(j * BKV - (s.L - s.n), 0) / p.tq;  // the first token that sees the first slot
+      r->q1 = cost;                                  // > q0: the last token sees every slot below L
+      mbar_arrive(&t.item_full[count % ITEMS]);
+      ++count;
+      k += take;
+      j += take;
+      if (j == tiles) {
+        j = 0;
+        ++g;
+      }
+    }
   }
-  const int per = p.c.Hkv / p.unit_heads;
-  const int64_t i = u - t.before[lo];
-  Unit r;
-  r.b = lo;
-  r.g0 = static_cast<int>(i % per) * p.unit_heads;
-  r.slot0 = static_cast<int>(i / per) * 2 * BKV;
-  const PlanSeq s = t.seq[lo];
-  r.q0 = max(r.slot0 - (s.L - s.n), 0) / p.tq;  // the first token that sees slot0
-  r.q1 = (s.n + p.tq - 1) / p.tq;
-  return r;
+  Unit *r = place();
+  if (r == nullptr) return;
+  r->more = 0;
+  mbar_arrive(&t.item_full[count % ITEMS]);
 }
 
 template <int D>
@@ -96,7 +149,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                          const __grid_constant__ Params p) {
   constexpr int CH = D / 64, TILE = CH * CHUNK;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *sQ = smem, *sK = smem + 2 * TILE;  // 2 Q tiles; 2 stages of 2 K tiles
+  uint8_t *sQ = smem, *sK = smem + 2 * TILE;  // a ring of 2 Q tiles; the unit's K tiles
   Tail &t = *reinterpret_cast<Tail *>(smem + 6 * TILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int *abort_flag = &t.abort_flag;
@@ -109,13 +162,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&t.q_full[i], 1);
       mbar_init(&t.q_empty[i], 1);
+    }
+    for (int i = 0; i < WG; ++i) {
       mbar_init(&t.k_full[i], 1);
       mbar_init(&t.k_empty[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
       mbar_init(&t.s_full[i], 1);
-      mbar_init(&t.s_free[i], 4);  // one arrival per warp
-      mbar_init(&t.lse_full[i], 4);
+      mbar_init(&t.s_free[i], 4);  // here and below: one arrival per warp
+      mbar_init(&t.lse_full[2 * i], 4);
+      mbar_init(&t.lse_full[2 * i + 1], 4);
+    }
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(&t.item_full[i], 1);
+      mbar_init(&t.item_empty[i], 18);  // a lane of every other warp that takes part
     }
     mbar_init(&t.drain, 1);
     t.abort_flag = 0;
@@ -137,8 +195,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
       const int b = b0 + lane;
       int64_t x = 0;
-      if (b < p.c.B && t.seq[b].n > 0)
-        x = static_cast<int64_t>((t.seq[b].L + 2 * BKV - 1) / (2 * BKV)) * (p.c.Hkv / p.unit_heads);
+      if (b < p.c.B)
+        x = static_cast<int64_t>(k_tiles(t.seq[b].L)) * (p.c.Hkv / p.unit_heads) * q_tiles(t.seq[b].n, p.tq);
       int64_t incl = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -153,189 +211,198 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = t.tmem;
-  const int64_t units = t.before[p.c.B];
+  const uint32_t tmem = uniform(t.tmem);
+  // The i-th unit for this warp, or null behind the last one (or on the way
+  // out); give_back lets warp 3 reuse its place.
+  auto take = [&](int i) -> const Unit * {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_long(&t.item_full[i % ITEMS], (i / ITEMS) & 1, abort_flag,
+                                                           p.status, p.wait_ns, 0x6Fu));
+    const Unit *un = &t.item[i % ITEMS];
+    return ok && uniform(un->more) ? un : nullptr;
+  };
+  auto give_back = [&](int i) { mbar_arrive_warp(&t.item_empty[i % ITEMS]); };
 
   if (warp == 0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
     const int page = 1 << p.c.page_shift, rows = min(page, BKV), boxes = BKV / rows;
     const bool mine = lane < boxes * CH;
     const int box = lane / CH, ch = lane % CH;
-    int qc = 0, kc = 0;
-    uint32_t q_issued = 0, q_par = 0, k_issued = 0, k_par = 0;
+    int qc = 0;
+    uint32_t q_issued = 0, q_par = 0, k_issued = 0, k_par = 0;  // k_par: the parity of each K tile's next phase
     bool ok = true;
     auto wait_all = [&](uint64_t *bar, uint32_t parity, uint32_t where) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns, where));
     };
-    for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const Unit un = unit_at(t, p, u);
-      const int L = t.seq[un.b].L;
-      int at[2];  // the pages of this lane's boxes, the same for every head; outside the tensor where there is none
-      for (int x = 0; x < 2; ++x) {
-        const int slot = un.slot0 + x * BKV + box * rows;
-        at[x] = p.c.num_pages;
-        if (mine && slot < L) {
-          const int n = paged_page(p.c.table, p.c.table_stride, p.c.num_pages, un.b, slot >> p.c.page_shift, p.status);
-          if (n >= 0) at[x] = n;
+    for (int i = 0; ok; ++i) {
+      const Unit *un = take(i);
+      if (!un) break;
+      const int L = un->L, g0 = un->g0, q0 = uniform(un->q0), q1 = uniform(un->q1), slot0 = un->slot0, b = un->b;
+      const int first = un->first, tiles = uniform(un->tiles);
+      give_back(i);
+      int at[WG];  // the pages of this lane's boxes, the same for every head; outside the tensor where there is none
+#pragma unroll
+      for (int w = 0; w < WG; ++w) {
+        const int slot = slot0 + w * BKV + box * rows;
+        at[w] = p.c.num_pages;
+        if (mine && w < tiles && slot < L) {
+          const int n = paged_page(p.c.table, p.c.table_stride, p.c.num_pages, b, slot >> p.c.page_shift, p.status);
+          if (n >= 0) at[w] = n;
         }
       }
-      if (un.q0 >= un.q1) continue;
-      for (int h = 0; ok && h < p.unit_heads; ++h, ++kc) {
-        const int g = un.g0 + h, st = kc & 1;
-        const uint32_t ph = (kc >> 1) & 1;
-        ok = wait_all(&t.k_empty[st], ph ^ 1u, 0x61u);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&t.k_full[st], 2 * TILE);
-        __syncwarp();
-        if (mine)
-          for (int x = 0; x < 2; ++x)
-            tma_load_4d(sK + (2 * st + x) * TILE + ch * CHUNK + box * rows * 128, &tmK, &t.k_full[st], ch * 64, g,
-                        (un.slot0 + x * BKV) & (page - 1), at[x]);
-        k_issued |= 1u << st;
-        k_par = (k_par & ~(1u << st)) | (ph << st);
-        for (int q = un.q0; q < un.q1; ++q, ++qc) {
+      for (int h = 0; ok && h < p.unit_heads; ++h) {
+        const int g = g0 + h;
+#pragma unroll
+        for (int w = 0; w < WG; ++w) {
+          if (w >= tiles || !ok) break;
+          ok = wait_all(&t.k_empty[w], ((k_par >> w) & 1u) ^ 1u, 0x61u);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&t.k_full[w], TILE);
+          __syncwarp();
+          if (mine)
+            tma_load_4d(sK + w * TILE + ch * CHUNK + box * rows * 128, &tmK, &t.k_full[w], ch * 64, g,
+                        (slot0 + w * BKV) & (page - 1), at[w]);
+          k_issued |= 1u << w;
+          k_par ^= 1u << w;
+        }
+        for (int q = q0; ok && q < q1; ++q, ++qc) {
           const int qs = qc & 1;
           const uint32_t qph = (qc >> 1) & 1;
           ok = wait_all(&t.q_empty[qs], qph ^ 1u, 0x62u);
           if (!ok) break;
           if (lane == 0) {
             mbar_arrive_expect_tx(&t.q_full[qs], p.tq * p.G * D * 2);
-            for (int i = 0; i < CH; ++i)
-              tma_load_3d(sQ + qs * TILE + i * CHUNK, &tmQ, &t.q_full[qs], i * 64, g * p.G,
-                          t.first[un.b] + q * p.tq);
+            for (int e = 0; e < CH; ++e)
+              tma_load_3d(sQ + qs * TILE + e * CHUNK, &tmQ, &t.q_full[qs], e * 64, g * p.G, first + q * p.tq);
           }
           q_issued |= 1u << qs;
           q_par = (q_par & ~(1u << qs)) | (qph << qs);
         }
       }
     }
-    if (*abort_flag && lane == 0)
-      for (int i = 0; i < 2; ++i) {
+    if (*abort_flag && lane == 0) {
+      for (int i = 0; i < 2; ++i)
         if (q_issued & (1u << i)) mbar_drain(&t.q_full[i], (q_par >> i) & 1u, p.status);
-        if (k_issued & (1u << i)) mbar_drain(&t.k_full[i], (k_par >> i) & 1u, p.status);
-      }
+      for (int i = 0; i < WG; ++i)
+        if (k_issued & (1u << i)) mbar_drain(&t.k_full[i], ((k_par >> i) & 1u) ^ 1u, p.status);
+    }
     __syncwarp();
   } else if (warp == 1) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
     constexpr uint32_t idesc = idesc_bf16_f32(BKV, 128, 0, 0);
-    int qc = 0, kc = 0;
+    int qc = 0;
+    uint32_t k_par = 0, s_par = 0;  // per K tile: parity of its next load, of its next S
     bool ok = true;
     auto wait_all = [&](uint64_t *bar, uint32_t parity, uint32_t where) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns, where));
     };
-    for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const Unit un = unit_at(t, p, u);
-      if (un.q0 >= un.q1) continue;
-      for (int h = 0; ok && h < p.unit_heads; ++h, ++kc) {
-        const int st = kc & 1;
-        ok = wait_all(&t.k_full[st], (kc >> 1) & 1, 0x63u);
-        for (int q = un.q0; ok && q < un.q1; ++q, ++qc) {
-          const int qs = qc & 1, buf = qc & 1;
-          const uint32_t ph = (qc >> 1) & 1;
-          ok = wait_all(&t.q_full[qs], ph, 0x64u);
+    for (int i = 0; ok; ++i) {
+      const Unit *un = take(i);
+      if (!un) break;
+      const int n = uniform(un->q1 - un->q0), tiles = uniform(un->tiles);
+      give_back(i);
+      for (int h = 0; ok && h < p.unit_heads; ++h) {
+        for (int q = 0; ok && q < n; ++q, ++qc) {
+          const int qs = qc & 1;
+          ok = wait_all(&t.q_full[qs], (qc >> 1) & 1, 0x64u);
           const uint32_t q_addr = smem_u32(sQ + qs * TILE);
-          for (int x = 0; ok && x < 2; ++x) {
-            ok = wait_all(&t.s_free[2 * x + buf], ph ^ 1u, 0x65u);
+          for (int w = 0; ok && w < tiles; ++w) {
+            if (q == 0) ok = wait_all(&t.k_full[w], (k_par >> w) & 1u, 0x63u);
+            ok = ok && wait_all(&t.s_free[w], ((s_par >> w) & 1u) ^ 1u, 0x65u);
             if (!ok) break;
+            s_par ^= 1u << w;
             tc_fence_after();
-            const uint32_t k_addr = smem_u32(sK + (2 * st + x) * TILE);
+            const uint32_t k_addr = smem_u32(sK + w * TILE);
 #pragma unroll
             for (int kk = 0; kk < 4 * CH; ++kk) {
               const uint64_t a = sdesc_k_sw128(k_addr + (kk >> 2) * CHUNK) + 2 * (kk & 3);
               const uint64_t b = sdesc_k_sw128(q_addr + (kk >> 2) * CHUNK) + 2 * (kk & 3);
-              mma_bf16_ss_w(tmem + x * 256 + buf * 128, a, b, idesc, kk > 0);
+              mma_bf16_ss_w(tmem + w * 128, a, b, idesc, kk > 0);
             }
-            tc_commit_w(&t.s_full[2 * x + buf]);
+            tc_commit_w(&t.s_full[w]);
+            if (q + 1 == n) tc_commit_w(&t.k_empty[w]);
           }
           if (ok) tc_commit_w(&t.q_empty[qs]);
         }
-        if (ok) tc_commit_w(&t.k_empty[st]);
+        k_par ^= (1u << tiles) - 1u;
       }
     }
     tc_commit_w(&t.drain);
     mbar_drain(&t.drain, 0, p.status);
     __syncwarp();
   } else if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));  // idle
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
+    if (warp == 3 && lane == 0) walk(t, p);  // warp 2 is idle
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_HIGH));
-    const int x = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16) + x * 256;
-    const uint64_t cc = f2pack(p.scale_log2, p.scale_log2);
-    const int rt = r / p.G, rh = r - rt * p.G;  // the token and head of Q row r (this thread fetches its lse)
-    int qc = 0;
+    const int wg = (warp - 4) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16) + wg * 128;
+    const float c2 = p.scale_log2;
+    const int rt = r / p.G, rh = r - rt * p.G;  // token and head of Q row r, whose lse this thread fetches
+    uint32_t sc = 0;                            // S tiles of this warpgroup so far
     bool ok = true;
-    for (int64_t u = blockIdx.x; ok && u < units; u += gridDim.x) {
-      const Unit un = unit_at(t, p, u);
-      if (un.q0 >= un.q1) continue;
-      const PlanSeq s = t.seq[un.b];
-      const int slot = un.slot0 + x * BKV + r, base = s.L - s.n;
-      uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+    for (int i = 0; ok; ++i) {
+      const Unit *un = take(i);
+      if (!un) break;
+      const bool on = wg < un->tiles;
+      const int n = un->n, L = un->L, q0 = un->q0, q1 = un->q1, g0 = un->g0, first = un->first;
+      const int slot = un->slot0 + wg * BKV + r, base = L - n;
+      float *w = p.out + (static_cast<int64_t>(un->b) * p.out_heads + (p.out_heads == 1 ? 0 : g0)) * p.out_stride + slot;
+      give_back(i);
+      if (!on) continue;
+      const float old = p.add && slot < L ? *w : 0.f;
+      // lse of this thread's row of Q tile q, fetched a tile ahead
+      auto lse_of = [&](int h, int q) -> float {
+        const int tok = q * p.tq + rt;
+        if (rt >= p.tq || tok >= n) return 0.f;
+        const float l = __ldg(p.lse + static_cast<int64_t>(first + tok) * p.Hq + (g0 + h) * p.G + rh);
+        return l == -INFINITY ? 0.f : -LOG2E * l;  // a row that sees nothing: every column of it is masked
+      };
+      float next = lse_of(0, q0), sum[4] = {0.f, 0.f, 0.f, 0.f};
       for (int h = 0; ok && h < p.unit_heads; ++h) {
-        const int head = (un.g0 + h) * p.G + rh;
-        auto lse_of = [&](int q) -> float {
-          const int tok = q * p.tq + rt;
-          if (q >= un.q1 || rt >= p.tq || tok >= s.n) return 0.f;
-          const float l = __ldg(p.lse + static_cast<int64_t>(t.first[un.b] + tok) * p.Hq + head);
-          return l == -INFINITY ? 0.f : -LOG2E * l;  // a row that sees nothing: every column of it is masked
-        };
-        float next = lse_of(un.q0);
-        for (int q = un.q0; q < un.q1; ++q, ++qc) {
-          const int buf = qc & 1;
-          const uint32_t ph = (qc >> 1) & 1;
-          reinterpret_cast<float *>(t.lse[x][buf])[r] = next;
-          mbar_arrive_warp(&t.lse_full[2 * x + buf]);
-          next = lse_of(q + 1);
-          ok = __all_sync(0xffffffffu, mbar_wait(&t.lse_full[2 * x + buf], ph, abort_flag, p.status, p.wait_ns, 0x66u));
+        for (int q = q0; q < q1; ++q, ++sc) {
+          uint64_t *lse_full = &t.lse_full[2 * wg + (sc & 1)];
+          t.lse[wg][sc & 1][r] = next;
+          mbar_arrive_warp(lse_full);
+          next = q + 1 < q1 ? lse_of(h, q + 1) : h + 1 < p.unit_heads ? lse_of(h + 1, q0) : 0.f;
+          ok = __all_sync(0xffffffffu, mbar_wait(lse_full, (sc >> 1) & 1, abort_flag, p.status, p.wait_ns, 0x66u));
           if (!ok) break;
-          ok = __all_sync(0xffffffffu, mbar_wait(&t.s_full[2 * x + buf], ph, abort_flag, p.status, p.wait_ns, 0x67u));
+          ok = __all_sync(0xffffffffu, mbar_wait(&t.s_full[wg], sc & 1, abort_flag, p.status, p.wait_ns, 0x67u));
           if (!ok) break;
           tc_fence_after();
-          uint32_t xr[128];
+          // rows of the tile that see the slot: tokens >= slot - base, up to the last one
+          const int lo = (slot - base - q * p.tq) * p.G, hi = min(p.tq, n - q * p.tq) * p.G;
+          const bool masked = __any_sync(0xffffffffu, lo > 0) || hi < 128;
+          const float4 *ls = reinterpret_cast<const float4 *>(t.lse[wg][sc & 1]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            tmem_ld32(lane_base + buf * 128 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(xr + 32 * c));
-          tmem_ld_wait();
-          tc_fence_before();
-          mbar_arrive_warp(&t.s_free[2 * x + buf]);
-          // rows of this tile that see the slot: tokens >= slot - base, up to the last one
-          const int lo = (slot - base - q * p.tq) * p.G, hi = min(p.tq, s.n - q * p.tq) * p.G;
-          if (__any_sync(0xffffffffu, lo > 0) || hi < 128) {
+          for (int half = 0; half < 2; ++half) {
+            uint32_t xr[64];
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c < lo || c >= hi) xr[c] = 0xff800000u;  // -inf
-          }
-          const ulonglong2 *ls = reinterpret_cast<const ulonglong2 *>(t.lse[x][buf]);
+            for (int c = 0; c < 2; ++c)
+              tmem_ld32(lane_base + half * 64 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(xr + 32 * c));
+            tmem_ld_wait();
+            if (half) {
+              tc_fence_before();
+              mbar_arrive_warp(&t.s_free[wg]);
+            }
+            if (masked) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const ulonglong2 l2 = ls[e];
+              for (int c = 0; c < 64; ++c)
+                if (half * 64 + c < lo || half * 64 + c >= hi) xr[c] = 0xff800000u;  // -inf
+            }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int pair = 2 * e + i;
-              const uint64_t a2 = f2fma(f2pack(__uint_as_float(xr[2 * pair]), __uint_as_float(xr[2 * pair + 1])), cc,
-                                        i ? l2.y : l2.x);
-              float a, b;
-              if (pair % 5 == 1 || pair % 5 == 3) {  // two fifths on the FMA pipe
-                exp2_fine2(a2, a, b);
-              } else {
-                f2unpack(a2, a, b);
-                a = ex2(a);
-                b = ex2(b);
-              }
-              sum[pair & 3] = f2add(sum[pair & 3], f2pack(a, b));
+            for (int e = 0; e < 16; ++e) {
+              const float4 l4 = ls[half * 16 + e];
+              sum[0] += ex2(fmaf(__uint_as_float(xr[4 * e]), c2, l4.x));
+              sum[1] += ex2(fmaf(__uint_as_float(xr[4 * e + 1]), c2, l4.y));
+              sum[2] += ex2(fmaf(__uint_as_float(xr[4 * e + 2]), c2, l4.z));
+              sum[3] += ex2(fmaf(__uint_as_float(xr[4 * e + 3]), c2, l4.w));
             }
           }
         }
       }
       if (!ok) break;
-      if (slot < s.L) {
-        float a, b, c, d;
-        f2unpack(f2add(sum[0], sum[1]), a, b);
-        f2unpack(f2add(sum[2], sum[3]), c, d);
-        const float add = (a + b) + (c + d);
-        float *w = p.out + (static_cast<int64_t>(un.b) * p.out_heads + (p.out_heads == 1 ? 0 : un.g0)) * p.out_stride + slot;
-        *w = p.add ? *w + add : add;
-      }
+      if (slot < L) *w = old + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
     }
   }
   __syncthreads();

@@ -26,6 +26,11 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 }
 
 
+// A value that all lanes hold, so that the compiler knows it too: loop counts
+// and ring places then live in uniform registers, where MMA descriptors have
+// to be (paged attention, 1024 rows over 16K slots: 246 us against 320).
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Number of a[0..n) that are <= v (a sorted ascending), by the whole warp:
 // each step samples 32 evenly spaced points, so 2^17 keys take 4 dependent
 // loads instead of 17.
