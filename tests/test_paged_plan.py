@@ -32,7 +32,7 @@ extern "C" int walk(int B, const int *n, const int *L, int w, int heads, int cta
     const int64_t x = plan_cut(total, nr, r);
     PlanCursor cur;
     plan_open(cur, seq.data(), before.data(), B, w, heads, x, plan_cut(total, nr, r + 1) - x);
-    cuts[r] = PlanCut{total, nr, cur.b, cur.p, cur.g, cur.off, cur.c};
+    cuts[r] = PlanCut{total, nr, cur.b, cur.p, cur.g, cur.off, cur.c, n[cur.b], L[cur.b], 0};
     PlanPiece pc;
     while (plan_next(cur, seq.data(), B, w, heads, pc)) {
       if (count == cap) return -1;
@@ -52,7 +52,7 @@ extern "C" void tiles_of(int off, int end, int c, int tiles, int *out) { plan_ti
 
 
 class Cut(C.Structure):
-    _fields_ = [("total", C.c_int64)] + [(n, C.c_int) for n in ("nr", "b", "p", "g", "off", "c")]
+    _fields_ = [("total", C.c_int64)] + [(n, C.c_int) for n in ("nr", "b", "p", "g", "off", "c", "n", "L", "first")]
 
 
 @pytest.fixture(scope="module")

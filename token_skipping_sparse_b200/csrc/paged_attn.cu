@@ -916,7 +916,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (rg < nr && cut.total > 0) {
       PlanCursor cur;
       plan_open(cur, t.seq, t.before, p.c.B, 2 * p.tq, heads, plan_cut(cut.total, nr, rg), 1);
-      cut = PlanCut{cut.total, nr, cur.b, cur.p, group * t.group_heads + cur.g, cur.off, cur.c};
+      const PlanSeq s = t.seq[cur.b];
+      cut = PlanCut{cut.total, nr,    cur.b, cur.p, group * t.group_heads + cur.g, cur.off, cur.c, s.n, s.L,
+                    t.first[cur.b]};
     }
     p.cuts[group * gridDim.x + rg] = cut;
   }
@@ -929,10 +931,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Joins the pieces of the unit whose first cut is in front of range
 // blockIdx.x + 1 of group blockIdx.y: O = sum_i 2^(m_i - m) O_i / sum_i
-// 2^(m_i - m) l_i, the pieces in order, one warp per row.  Launched while the
-// attention still runs (its CTAs take the places of those that ended), and
-// waits for it.
+// 2^(m_i - m) l_i, the pieces in order.  A chain of dependent loads (the cut,
+// the statistics, the rows), so a warp takes JOIN_ROWS rows at once.  Launched
+// while the attention still runs (its CTAs take the places of those that
+// ended), and waits for it.
 constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_ROWS = 4;
 
 template <int D>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __grid_constant__ Params p, int ctas) {
@@ -943,11 +947,9 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PlanCut cut = p.cuts[group * ctas + range];
   if (!plan_first_cut(cut, range)) return;
-  int first, n;
-  packed_span(p.cu, p.T, cut.b, nullptr, first, n);
-  const PlanSeq s{n, paged_len(p.c, cut.b, nullptr)};
+  const PlanSeq s{cut.n, cut.L};
   const int w = 2 * p.tq, tok0 = cut.p * w, g = cut.g;
-  const int rows = min(w, n - tok0) * p.G;
+  const int rows = min(w, s.n - tok0) * p.G;
   const int tiles = (plan_visible(s, tok0 + w) + BKV - 1) / BKV;
   const int lane = threadIdx.x & 31;
   // where piece i of this unit lies, or -1 if it has no tile; `last`: whether it ends the unit
@@ -959,61 +961,82 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __
     plan_tiles(off, end, cut.c, tiles, t0, t1);
     return t0 < t1 ? ((static_cast<int64_t>(group) * ctas + rg) * 2 + slot) * SLOT_ROWS : -1;
   };
-  for (int row = blockIdx.z * JOIN_WARPS + (threadIdx.x >> 5); row < rows; row += static_cast<int>(gridDim.z) * JOIN_WARPS) {
-    float m = -INFINITY, l = 0.f, acc[E];
+  const int warps = static_cast<int>(gridDim.z) * JOIN_WARPS;
+  for (int row0 = blockIdx.z * JOIN_WARPS + (threadIdx.x >> 5); row0 < rows; row0 += warps * JOIN_ROWS) {
+    float m[JOIN_ROWS], l[JOIN_ROWS], acc[JOIN_ROWS][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int q = 0; q < JOIN_ROWS; ++q) {
+      m[q] = -INFINITY;
+      l[q] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[q][e] = 0.f;
+    }
     bool done = false;
     for (int i0 = 0; !done; i0 += 32) {  // 32 pieces at a time: lane i has the statistics of piece i0 + i
       bool last;
       const int64_t at = piece(i0 + lane, last);
       done = __any_sync(0xffffffffu, last);
-      const float2 ml = at >= 0 ? p.part_ml[at + row] : make_float2(-INFINITY, 0.f);
-      float top = ml.x;
+      const int pieces = 32 - __clz(__ballot_sync(0xffffffffu, at >= 0));
+      float2 ml[JOIN_ROWS];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float mn = max_nan(m, top), zero = mn == -INFINITY ? 0.f : mn;
-      const float keep = ex2(m - zero), f = ex2(ml.x - zero);
-      float part = ml.y * f;
+      for (int q = 0; q < JOIN_ROWS; ++q) {
+        const int row = row0 + q * warps;
+        ml[q] = at >= 0 && row < rows ? p.part_ml[at + row] : make_float2(-INFINITY, 0.f);
+      }
+      float f[JOIN_ROWS];
+      uint32_t live[JOIN_ROWS];  // pieces of which the row sees nothing are skipped: their O may be anything
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-      l = l * keep + part;
-      m = mn;
+      for (int q = 0; q < JOIN_ROWS; ++q) {
+        float top = ml[q].x;
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= keep;
-      // pieces of which this row sees nothing are skipped: their O may be anything
-      const uint32_t live = __ballot_sync(0xffffffffu, at >= 0 && ml.x != -INFINITY);
-      const int pieces = 32 - __clz(live);
-      for (int j = 0; j < pieces; j += 4) {  // four pieces' rows in flight together
-        Vec v[4];
-        float fj[4];
+        for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float mn = max_nan(m[q], top), zero = mn == -INFINITY ? 0.f : mn, keep = ex2(m[q] - zero);
+        f[q] = ex2(ml[q].x - zero);
+        float part = ml[q].y * f[q];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int i = (j + q) & 31;
-          fj[q] = __shfl_sync(0xffffffffu, f, i);
-          const int64_t from = __shfl_sync(0xffffffffu, at, i);
-          const bool on = j + q < pieces && ((live >> i) & 1u);
-          if (!on) fj[q] = 0.f;
-          if (on) v[q] = *reinterpret_cast<const Vec *>(p.part_o + (from + row) * D + lane * E);
-          else v[q] = Vec{};
+        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        l[q] = l[q] * keep + part;
+        m[q] = mn;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[q][e] *= keep;
+        live[q] = __ballot_sync(0xffffffffu, ml[q].x != -INFINITY);
+      }
+#pragma unroll 2
+      for (int j = 0; j < pieces; ++j) {
+        const int64_t from = __shfl_sync(0xffffffffu, at, j);
+        Vec v[JOIN_ROWS];
+#pragma unroll
+        for (int q = 0; q < JOIN_ROWS; ++q) {
+          v[q] = Vec{};
+          if ((live[q] >> j) & 1u)
+            v[q] = *reinterpret_cast<const Vec *>(p.part_o + (from + row0 + q * warps) * D + lane * E);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < JOIN_ROWS; ++q) {
+          const float fj = __shfl_sync(0xffffffffu, f[q], j);
+          if ((live[q] >> j) & 1u) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(reinterpret_cast<const float *>(&v[q])[e], fj[q], acc[e]);
+            for (int e = 0; e < E; ++e) acc[q][e] = fmaf(reinterpret_cast<const float *>(&v[q])[e], fj, acc[q][e]);
+          }
+        }
       }
     }
-    const int tok = first + tok0 + row / p.G, head = g * p.G + row % p.G;
-    const bool none = plan_visible(s, tok0 + row / p.G + 1) == 0;
-    const float inv = none ? 0.f : 1.f / l;
-    __nv_bfloat16 *o = p.o + tok * p.o_stride + head * D + lane * E;
-    uint32_t packed[E / 2];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) packed[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (E == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(packed[0], packed[E / 2 - 1]);
-    else *reinterpret_cast<uint32_t *>(o) = packed[0];
-    if (lane == 0 && p.lse)
-      p.lse[static_cast<int64_t>(tok) * p.Hq + head] = none ? -INFINITY : (m + log2f(l)) * LN2;
+    for (int q = 0; q < JOIN_ROWS; ++q) {
+      const int row = row0 + q * warps;
+      if (row >= rows) break;
+      const int tok = cut.first + tok0 + row / p.G, head = g * p.G + row % p.G;
+      const bool none = plan_visible(s, tok0 + row / p.G + 1) == 0;
+      const float inv = none ? 0.f : 1.f / l[q];
+      __nv_bfloat16 *o = p.o + tok * p.o_stride + head * D + lane * E;
+      uint32_t packed[E / 2];
+#pragma unroll
+      for (int e = 0; e < E; e += 2) packed[e / 2] = pack_bf16x2(acc[q][e] * inv, acc[q][e + 1] * inv);
+      if (E == 4) *reinterpret_cast<uint2 *>(o) = make_uint2(packed[0], packed[E / 2 - 1]);
+      else *reinterpret_cast<uint32_t *>(o) = packed[0];
+      if (lane == 0 && p.lse)
+        p.lse[static_cast<int64_t>(tok) * p.Hq + head] = none ? -INFINITY : (m[q] + log2f(l[q])) * LN2;
+    }
   }
 }
 
@@ -1047,8 +1070,9 @@ spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   note_launch();
   SPTS_CUDA_TRY(cudaGetLastError());
   if (ctas > 1) {
-    // CTAs per unit: two rows of the largest window for each warp
-    const int most = (p.T < 2 * p.tq ? p.T : 2 * p.tq) * p.G, split = FEW ? 1 : (most + 2 * JOIN_WARPS - 1) / (2 * JOIN_WARPS);
+    // CTAs per unit: one turn of its warps for the largest window
+    const int most = (p.T < 2 * p.tq ? p.T : 2 * p.tq) * p.G, turn = JOIN_WARPS * JOIN_ROWS;
+    const int split = FEW ? 1 : (most + turn - 1) / turn;
     SPTS_TRY(launch_behind(paged_combine_kernel<D>, dim3(ctas - 1, p.max_groups, split), 32 * JOIN_WARPS, s, p, ctas));
   }
   return SPTS_OK;

@@ -190,6 +190,7 @@ struct PlanCut {
   int nr;         // its ranges (0: this range is not one of them)
   int b, p, g;    // the unit at the cut (g: counted over all heads)
   int off, c;     // how far inside it the cut is (0: between two units), and the unit's cost
+  int n, L, first;  // its sequence: new tokens, cached tokens, first packed row
 };
 
 // Whether the cut in front of range r is the first one inside its unit.
