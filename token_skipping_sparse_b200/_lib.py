@@ -403,10 +403,11 @@ def _want(t, dtype, dims, device, what):
 
 def _packed(t, dev, what):
     """Row stride of packed tokens [T, H, d] whose heads lie as in a contiguous tensor."""
-    if t.dtype is not _BF or t.dim() != 3 or t.device != dev:
+    st = t.stride()
+    if t.dtype is not _BF or len(st) != 3 or t.get_device() != dev.index:
         _want(t, _BF, 3, dev, what)
     T, H, d = t.shape
-    row, head, col = t.stride()
+    row, head, col = st
     if col != 1 or (head != d and H > 1):
         raise ValueError(f"{what}: heads and columns must be contiguous")
     return row if T > 1 else H * d
@@ -420,21 +421,23 @@ def _table_stride(t, what):
 
 
 def _paged(k_pages, v_pages, page_table, seq_lens, dev):
+    index = -1 if dev.index is None else dev.index
+    shape, table = k_pages.shape, page_table.shape
     if not (k_pages.dtype is _BF and v_pages.dtype is _BF and page_table.dtype is _I32 and seq_lens.dtype is _I32 and
-            k_pages.dim() == 4 and page_table.dim() == 2 and seq_lens.dim() == 1 and k_pages.device == dev and
-            v_pages.device == dev and page_table.device == dev and seq_lens.device == dev):
+            len(shape) == 4 and len(table) == 2 and seq_lens.dim() == 1 and k_pages.get_device() == index and
+            v_pages.get_device() == index and page_table.get_device() == index and seq_lens.get_device() == index):
         _want(k_pages, _BF, 4, dev, "k_pages")
         _want(v_pages, _BF, 4, dev, "v_pages")
         _want(page_table, _I32, 2, dev, "page_table")
         _want(seq_lens, _I32, 1, dev, "seq_lens")
-    n, page, Hkv, d = shape = k_pages.shape
+    n, page, Hkv, d = shape
     st = k_pages.stride()
     if v_pages.shape != shape or v_pages.stride() != st or \
             (st[1:] != (Hkv * d, d, 1) and any(k > 1 and x != y for k, x, y in zip(shape[1:], st[1:], (Hkv * d, d, 1)))):
         raise ValueError("k_pages and v_pages must be alike, and contiguous inside a page")
-    rows, width = page_table.shape
+    rows, width = table
     row, col = page_table.stride()
-    B, = seq_lens.shape
+    B = seq_lens.shape[0]
     if rows != B or (B > 1 and seq_lens.stride(0) != 1) or (col != 1 and width > 1):
         raise ValueError("page_table and seq_lens need one row and one contiguous entry per sequence")
     c = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), n, st[0] if n > 1 else 0, page, B, page_table.data_ptr(),
@@ -445,7 +448,7 @@ def _paged(k_pages, v_pages, page_table, seq_lens, dev):
 
 def _vector(t, n, dev, what):
     """Address of n contiguous int32 entries."""
-    if t.dtype is not _I32 or t.dim() != 1 or t.device != dev or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not _I32 or t.shape != (n,) or t.get_device() != dev.index or (n > 1 and t.stride(0) != 1):
         _want(t, _I32, 1, dev, what)
         raise ValueError(f"{what}: need {n} contiguous entries, got {tuple(t.shape)} with strides {t.stride()}")
     return t.data_ptr()
@@ -453,7 +456,7 @@ def _vector(t, n, dev, what):
 
 def _scores(weights, c, Hkv, dev, what):
     """(Hs, stride between rows [b, hs], slots) of a weights tensor."""
-    if weights.dtype is not _F32 or weights.dim() != 3 or weights.device != dev:
+    if weights.dtype is not _F32 or weights.dim() != 3 or weights.get_device() != dev.index:
         _want(weights, _F32, 3, dev, what)
     B, Hs, n = weights.shape
     sb, sh, sn = weights.stride()
@@ -472,7 +475,8 @@ def _own_ws(ws, nbytes, dev):
         return _want(ws, torch.uint8, 1, dev, "ws")
     if torch.cuda.is_current_stream_capturing():
         raise ValueError("pass a workspace of your own (ws) while a graph is captured")
-    return workspace(nbytes, dev)
+    t = _ws_cache.get(dev)
+    return t if t is not None and t.numel() >= nbytes else workspace(nbytes, dev)
 
 
 def _elsewhere(dev, who):
