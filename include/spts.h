@@ -330,6 +330,7 @@ SPTS_API size_t spts_select_sequential_workspace(int64_t Nc);
  * Slots are in the order of the tokens; K rows carry their RoPE, so after an
  * eviction slot numbers need not be positions.  A page must not belong to two
  * sequences of a call that writes to it.
+ * All buffers of a call are on the device that is current when it is made.
  * The lengths, offsets and page numbers live on the device: a length outside
  * [0, max_pages * page_size], an offset outside [0, T] or below the one
  * before it, or a page number outside [0, num_pages) raises the INVALID flag
@@ -371,8 +372,8 @@ SPTS_API spts_status spts_cache_append(const spts_attn_desc *a, const spts_paged
  * sequence b (its own token, which must be cached already, and all before it;
  * n == 1 is a step of decoding, n == L a whole prompt).
  *   q, o     [T, Hq, d] bf16, rows q_stride / o_stride elements apart
- *            (multiples of 8, 0: Hq * d); rows from cu_q[B] on are not read
- *            and left as they are
+ *            (multiples of 8, 0: Hq * d); o must not overlap q; rows from
+ *            cu_q[B] on are not read and left as they are
  *   cu_q     [B + 1] int32 ascending from 0
  *   lse      [T, Hq] fp32 out, or NULL: ln of the sum over the visible slots
  *            of exp(scale * q . k) (-inf for a row that sees none)
@@ -380,7 +381,9 @@ SPTS_API spts_status spts_cache_append(const spts_attn_desc *a, const spts_paged
  *            weights[b, g, t] += the softmax weight that slot t received,
  *            summed over the sequence's new tokens and the query heads of KV
  *            head g (all query heads with Hs = 1), in a fixed order
- *            w_stride >= max_pages * page_size; slots from L on are left
+ *            w_stride >= max_pages * page_size; slots from L on are left;
+ *            where a row or key is not finite, what its sequence gets is
+ *            unspecified
  * The same call gives the same bits every time; the last bits of a sequence's
  * rows may depend on the lengths of the others (where the work is divided).
  * A row that sees no slot is written as 0.  Slots from L on may hold

@@ -132,6 +132,8 @@ CASES = {
     "a group as wide as a tile": ([3, 2], [30, 129], 128, 1, 64, 16),
     "nothing new": ([0, 0, 1], [40, 0, 10], 4, 2, 128, 16),
     "no sequence has anything": ([0, 0], [0, 0], 4, 2, 128, 16),
+    "steps beside chunks": ([1] * 24 + [30, 40], [9 * i for i in range(24)] + [200, 70], 8, 2, 128, 16),
+    "as many sequences as there may be": ([1, 0, 2, 1] * 256, [i % 19 for i in range(1024)], 4, 2, 64, 16),
     "many short ones": ([1, 2, 0, 3] * 12, [i % 37 for i in range(48)], 4, 2, 64, 16),
 }
 
@@ -393,6 +395,79 @@ def test_bad_pages_and_missing_slots_are_flagged_by_append_and_evict():
         S.check_device_status()
 
 
+def test_waits_that_run_out_end_the_call_with_a_status():
+    # (large enough for waits that the barrier's own patience does not cover)
+    c = Cache([4000, 90], 16, 8, 128, seed=42)
+    cu, q = packed([2000, 1], 32, 128, 43)
+    w = torch.zeros(2, 8, c.table.shape[1] * 16, device="cuda")
+    clean = S.spts_paged_attention(q, *c.args(), i32(cu), weights=w.clone())
+    S.check_device_status()
+    limit = S.get_wait_limit_ns()
+    S.set_wait_limit_ns(0)
+    try:
+        S.spts_paged_attention(q, *c.args(), i32(cu), weights=w.clone())
+        with pytest.raises(S.SptsError, match="gave up"):
+            S.check_device_status()
+    finally:
+        S.set_wait_limit_ns(limit)
+    assert torch.equal(S.spts_paged_attention(q, *c.args(), i32(cu), weights=w), clean)
+    S.check_device_status()
+
+
+# ------------------------------------------------------------------ sizes
+def test_pages_beyond_32_bit_offsets():
+    # 2.2e9 elements of K and of V; the sequence's pages are the last ones
+    page, Hkv, d, n_pages = 256, 8, 128, 8400
+    k, v = (torch.empty(n_pages, page, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert k.numel() > 2 ** 31
+    table = i32([[n_pages - 1, n_pages - 3, n_pages - 5]])
+    L = 600
+    cu, kv = packed([L], Hkv, d, 44, gain=1.0)
+    _, q = packed([7], 8, d, 45)
+    S.spts_cache_append(kv, kv * 0.5, k, v, table, i32([L]), i32([0, L]))
+    o = S.spts_paged_attention(q, k, v, table, i32([L]), i32([0, 7]))
+    small = [x[[n_pages - 1, n_pages - 3, n_pages - 5]].contiguous() for x in (k, v)]
+    own = i32([[0, 1, 2]])
+    assert torch.equal(small[0].view(-1, Hkv, d)[:L], kv)
+    assert torch.equal(o, S.spts_paged_attention(q, *small, own, i32([L]), i32([0, 7])))
+    w = torch.rand(1, Hkv, 3 * page, device="cuda")
+    lens, w_out, kept = S.spts_cache_evict(k, v, table, i32([L]), w, 200, dst_table=i32([[n_pages - 2]]), kept=True)
+    S.check_device_status()
+    for g in range(Hkv):
+        assert torch.equal(k[n_pages - 2, :200, g], kv[kept[0, g].long(), g])
+
+
+def test_evict_of_rows_too_long_to_hold():
+    # 410000 slots: a cluster's shared memory does not hold their keys
+    page, d, L, keep = 256, 64, 410003, 1500
+    n_pages = -(-L // page)
+    k = torch.randn(n_pages + 6, page, 1, d, device="cuda").bfloat16()
+    v = torch.randn(n_pages + 6, page, 1, d, device="cuda").bfloat16()
+    w = torch.randint(0, 5000, (1, 1, n_pages * page), device="cuda").float()  # ties at the threshold
+    table = torch.arange(n_pages, dtype=I32, device="cuda")[None]
+    dst = torch.arange(n_pages, n_pages + 6, dtype=I32, device="cuda")[None]
+    lens, w_out, kept = S.spts_cache_evict(k, v, table, i32([L]), w, keep, sink=3, recent=10, dst_table=dst, kept=True)
+    S.check_device_status()
+    x = w[0, 0, 3:L - 10].cpu().numpy()
+    order = np.argsort(-x, kind="stable")[:keep - 13] + 3
+    want = np.sort(np.concatenate((np.arange(3), order, np.arange(L - 10, L))))
+    assert np.array_equal(kept[0, 0].cpu().numpy(), want) and lens.tolist() == [keep]
+    idx = torch.from_numpy(want).cuda()
+    assert torch.equal(w_out[0, 0, :keep], w[0, 0, idx]) and not w_out[0, 0, keep:].any()
+    for x in (k, v):
+        assert torch.equal(x[n_pages:].view(-1, d)[:keep], x.view(-1, d)[idx])
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 3]])
+def test_weights_over_all_heads_with_a_wide_table(new):
+    # a page table row for 2.2 M slots: neither scores nor partial sums per head have scratch
+    c = Cache([300, 130], 16, 8, 64, seed=46)
+    wide = torch.full((2, 140000), -1, dtype=I32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    check_attention(c, new, 16, 8, 64, seed=47, each=False)
+
+
 # ------------------------------------------------------------------ streams, graphs, a run of all
 def test_two_streams_with_workspaces_of_their_own():
     cs = [Cache([700 + 50 * i, 90], 16, 2, 128, seed=31 + i) for i in range(2)]
@@ -470,6 +545,18 @@ def test_steps_of_decoding_under_a_budget_eager_and_captured():
     assert torch.equal(w[0], w[1]) and c.seq_lens.tolist() == [60, 26, 60]
     for a, b in ((caches[0].k, caches[1].k), (caches[0].v, caches[1].v)):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_tensors_on_another_device_are_refused():
+    c = Cache([20], 16, 2, 64, seed=48)
+    cu, q = packed([1], 4, 64, 49)
+    for args in ((c.k, c.v, c.table.cpu(), c.seq_lens), (c.k, c.v.cpu(), c.table, c.seq_lens)):
+        with pytest.raises(ValueError):
+            S.spts_paged_attention(q, *args, i32(cu))
+    with pytest.raises(ValueError, match="cu_q"):
+        S.spts_paged_attention(q, *c.args(), torch.tensor(cu, dtype=I32))
+    with pytest.raises(ValueError, match="weights"):
+        S.spts_paged_attention(q, *c.args(), i32(cu), weights=torch.zeros(1, 2, 16, device="cuda"))
 
 
 def test_capture_needs_a_workspace_of_the_callers():

@@ -31,8 +31,8 @@
 // both.  A unit with one (n <= tq: decoding) gives the even key tiles to x = 0
 // and the odd ones to x = 1, with the same Q, and joins the two at the end:
 // the softmax of one key tile runs beside the MMAs of the next either way.
-// P is rounded to bf16 for the product with V (half a step, 2^-9 of each
-// weight); S, the maxima, the sums and O stay in fp32.
+// P is rounded to bf16 for the product with V (half a step: 2^-8 of each
+// weight at most); S, the maxima, the sums and O stay in fp32.
 // All barrier waits are bounded (see sm100.cuh).
 #include <type_traits>
 
@@ -57,9 +57,9 @@ constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 constexpr float LN2 = 0.69314718055994530942f;
 // One column pair in POLY_EVERY takes its exp2 from the FMA pipe (exp2_poly2,
 // 1e-4, far below P's bf16 step) when the row sums serve the bf16 output
-// alone.  Where lse or weights are wanted all are the MUFU pipe's: a finer
-// polynomial for two fifths of them cost more registers than it gave (250
-// rows over 32K slots: 141 us against 134).
+// alone.  Where lse or weights are wanted all are the MUFU pipe's: a degree-5
+// polynomial (2.6e-7) for two fifths of them cost more registers than it gave
+// (250 rows over 32K slots: 141 us against 134).
 constexpr int POLY_EVERY = 3;
 
 template <int D>
@@ -183,7 +183,7 @@ __device__ __forceinline__ void tmem_st_rows16(uint32_t addr, const uint32_t (&r
 }
 
 __device__ __forceinline__ int heads_of(const Tail &t, const Params &p, int group) {
-  return min(t.group_heads, p.c.Hkv - group * t.group_heads);
+  return max(min(t.group_heads, p.c.Hkv - group * t.group_heads), 0);
 }
 
 // Warp 3, one lane: the pieces of this CTA's ranges, group after group.
@@ -612,7 +612,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (few && quad == 0) {
         // At most 16 rows: with a thread per row a warp would walk 128 columns
         // with most of its lanes idle, and the key tile would wait for it (one
-        // row over 128K slots: TODO us, against 103.6).
+        // row over 128K slots: 102.4 us against 103.6, with pages of 16 slots
+        // 115 against 132).
         const PlanSeq s{it->n, it->L};
         const int tok0 = it->tok0, left = s.n - tok0;
         const int lim_a = na < left ? plan_visible(s, tok0 + na + 1) : 0;

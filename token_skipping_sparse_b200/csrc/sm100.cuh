@@ -510,29 +510,6 @@ __device__ __forceinline__ void exp2_poly2(uint64_t x2, float &e0, float &e1) {
   e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(y1) << 23));
 }
 
-// The same with a degree-5 polynomial (relative error 2.6e-7, fp32 rounding
-// included; coefficients from exp2_poly_fit.py too), where the exponentials
-// serve an fp32 output.
-__device__ __forceinline__ void exp2_fine2(uint64_t x2, float &e0, float &e1) {
-  float a, b;
-  f2unpack(x2, a, b);
-  const uint64_t x = f2pack(fmaxf(a, -127.f), fmaxf(b, -127.f));
-  const uint64_t y = f2add(x, f2pack(12582912.f, 12582912.f));
-  const uint64_t j = f2add(y, f2pack(-12582912.f, -12582912.f));
-  const uint64_t f = f2fma(j, f2pack(-1.f, -1.f), x);
-  uint64_t p = f2fma(f2pack(0.0013381302123889327f, 0.0013381302123889327f), f,
-                     f2pack(0.00966636836528778f, 0.00966636836528778f));
-  p = f2fma(p, f, f2pack(0.055503811687231064f, 0.055503811687231064f));
-  p = f2fma(p, f, f2pack(0.2402234971523285f, 0.2402234971523285f));
-  p = f2fma(p, f, f2pack(0.6931471824645996f, 0.6931471824645996f));
-  p = f2fma(p, f, f2pack(1.0f, 1.0f));
-  float p0, p1, y0, y1;
-  f2unpack(p, p0, p1);
-  f2unpack(y, y0, y1);
-  e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(y0) << 23));
-  e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(y1) << 23));
-}
-
 // Byte offset of 16-byte unit `u` (0..7) of row `r` inside a 128-byte-swizzled
 // tile whose rows are 128 bytes (the layout TMA SWIZZLE_128B writes and UMMA
 // SW128 reads; the tile base must be 1024-byte aligned).

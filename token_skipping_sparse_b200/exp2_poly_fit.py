@@ -1,6 +1,5 @@
 """Derives the coefficients of the polynomial exp2 used by the reduced-attention
-softmax kernel (``exp2_poly2`` in csrc/sm100.cuh), and of the finer one where
-the exponentials serve an fp32 output (``exp2_fine2``).
+softmax kernel (``exp2_poly2`` in csrc/sm100.cuh).
 
 Method: range reduction to 2^x = 2^j * 2^f with j = round(x) and
 f = x - j in [-1/2, 1/2], then 2^f by the degree-3 polynomial with p(0) = 1
@@ -19,7 +18,6 @@ import numpy as np
 from scipy.optimize import linprog
 
 DEGREE = 3
-FINE_DEGREE = 5
 
 
 def fit(degree=DEGREE, n=4001):
@@ -40,15 +38,6 @@ def fit(degree=DEGREE, n=4001):
     return np.concatenate([[1.0], res.x[:-1]]), res.x[-1]
 
 
-def fit_fine(degree=FINE_DEGREE):
-    """p(0) = 1 again; the rest interpolates (2^f - 1) / f at the Chebyshev
-    points of [-1/2, 1/2], which is within a small factor of the minimax fit:
-    at this degree fp32 rounding, not the fit, sets the error."""
-    f = 0.5 * np.cos(np.pi * (2 * np.arange(degree) + 1) / (2 * degree))
-    c = np.linalg.solve(np.vander(f, degree, increasing=True), np.expm1(f * np.log(2.0)) / f)
-    return np.concatenate([[1.0], c])
-
-
 def horner_fp32(c, f):
     c = np.asarray(c, dtype=np.float32)
     f = np.asarray(f, dtype=np.float32)
@@ -64,10 +53,5 @@ if __name__ == "__main__":
     f = np.linspace(-0.5, 0.5, 200001, dtype=np.float32)
     err = np.abs(horner_fp32(c32, f).astype(np.float64) / 2.0 ** f.astype(np.float64) - 1.0).max()
     print(f"degree {DEGREE}: minimax relative error {t:.3e}; fp32 Horner {err:.3e}")
-    for i, a in enumerate(c32):
-        print(f"  c{i} = {float(a)!r}f  ({float(a).hex()})")
-    c32 = fit_fine().astype(np.float32)
-    err = np.abs(horner_fp32(c32, f).astype(np.float64) / 2.0 ** f.astype(np.float64) - 1.0).max()
-    print(f"degree {FINE_DEGREE}: fp32 Horner {err:.3e}")
     for i, a in enumerate(c32):
         print(f"  c{i} = {float(a)!r}f  ({float(a).hex()})")
