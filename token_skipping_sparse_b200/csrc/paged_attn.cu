@@ -937,9 +937,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 // while the attention still runs (its CTAs take the places of those that
 // ended), and waits for it.
 constexpr int JOIN_WARPS = 8;
-constexpr int JOIN_ROWS = 4;
 
-template <int D>
+template <int D, int ROWS, int DEEP>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __grid_constant__ Params p, int ctas) {
   const int range = blockIdx.x + 1, group = blockIdx.y;
   constexpr int E = D / 32;
@@ -963,10 +962,10 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __
     return t0 < t1 ? ((static_cast<int64_t>(group) * ctas + rg) * 2 + slot) * SLOT_ROWS : -1;
   };
   const int warps = static_cast<int>(gridDim.z) * JOIN_WARPS;
-  for (int row0 = blockIdx.z * JOIN_WARPS + (threadIdx.x >> 5); row0 < rows; row0 += warps * JOIN_ROWS) {
-    float m[JOIN_ROWS], l[JOIN_ROWS], acc[JOIN_ROWS][E];
+  for (int row0 = blockIdx.z * JOIN_WARPS + (threadIdx.x >> 5); row0 < rows; row0 += warps * ROWS) {
+    float m[ROWS], l[ROWS], acc[ROWS][E];
 #pragma unroll
-    for (int q = 0; q < JOIN_ROWS; ++q) {
+    for (int q = 0; q < ROWS; ++q) {
       m[q] = -INFINITY;
       l[q] = 0.f;
 #pragma unroll
@@ -978,16 +977,16 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __
       const int64_t at = piece(i0 + lane, last);
       done = __any_sync(0xffffffffu, last);
       const int pieces = 32 - __clz(__ballot_sync(0xffffffffu, at >= 0));
-      float2 ml[JOIN_ROWS];
+      float2 ml[ROWS];
 #pragma unroll
-      for (int q = 0; q < JOIN_ROWS; ++q) {
+      for (int q = 0; q < ROWS; ++q) {
         const int row = row0 + q * warps;
         ml[q] = at >= 0 && row < rows ? p.part_ml[at + row] : make_float2(-INFINITY, 0.f);
       }
-      float f[JOIN_ROWS];
-      uint32_t live[JOIN_ROWS];  // pieces of which the row sees nothing are skipped: their O may be anything
+      float f[ROWS];
+      uint32_t live[ROWS];  // pieces of which the row sees nothing are skipped: their O may be anything
 #pragma unroll
-      for (int q = 0; q < JOIN_ROWS; ++q) {
+      for (int q = 0; q < ROWS; ++q) {
         float top = ml[q].x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -1002,28 +1001,33 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __
         for (int e = 0; e < E; ++e) acc[q][e] *= keep;
         live[q] = __ballot_sync(0xffffffffu, ml[q].x != -INFINITY);
       }
-#pragma unroll 2
-      for (int j = 0; j < pieces; ++j) {
-        const int64_t from = __shfl_sync(0xffffffffu, at, j);
-        Vec v[JOIN_ROWS];
+      for (int j = 0; j < pieces; j += DEEP) {
+        Vec v[DEEP][ROWS];
 #pragma unroll
-        for (int q = 0; q < JOIN_ROWS; ++q) {
-          v[q] = Vec{};
-          if ((live[q] >> j) & 1u)
-            v[q] = *reinterpret_cast<const Vec *>(p.part_o + (from + row0 + q * warps) * D + lane * E);
-        }
+        for (int i = 0; i < DEEP; ++i) {
+          const int64_t from = __shfl_sync(0xffffffffu, at, (j + i) & 31);
 #pragma unroll
-        for (int q = 0; q < JOIN_ROWS; ++q) {
-          const float fj = __shfl_sync(0xffffffffu, f[q], j);
-          if ((live[q] >> j) & 1u) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[q][e] = fmaf(reinterpret_cast<const float *>(&v[q])[e], fj, acc[q][e]);
+          for (int q = 0; q < ROWS; ++q) {
+            v[i][q] = Vec{};
+            if (j + i < pieces && ((live[q] >> ((j + i) & 31)) & 1u))
+              v[i][q] = *reinterpret_cast<const Vec *>(p.part_o + (from + row0 + q * warps) * D + lane * E);
           }
         }
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i)
+#pragma unroll
+          for (int q = 0; q < ROWS; ++q) {
+            const float fi = __shfl_sync(0xffffffffu, f[q], (j + i) & 31);
+            if (j + i < pieces && ((live[q] >> ((j + i) & 31)) & 1u)) {
+#pragma unroll
+              for (int e = 0; e < E; ++e)
+                acc[q][e] = fmaf(reinterpret_cast<const float *>(&v[i][q])[e], fi, acc[q][e]);
+            }
+          }
       }
     }
 #pragma unroll
-    for (int q = 0; q < JOIN_ROWS; ++q) {
+    for (int q = 0; q < ROWS; ++q) {
       const int row = row0 + q * warps;
       if (row >= rows) break;
       const int tok = cut.first + tok0 + row / p.G, head = g * p.G + row % p.G;
@@ -1072,9 +1076,11 @@ spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   SPTS_CUDA_TRY(cudaGetLastError());
   if (ctas > 1) {
     // CTAs per unit: one turn of its warps for the largest window
-    const int most = (p.T < 2 * p.tq ? p.T : 2 * p.tq) * p.G, turn = JOIN_WARPS * JOIN_ROWS;
+    constexpr int ROWS = FEW ? 1 : 4, DEEP = FEW ? 8 : 2;
+    const int most = (p.T < 2 * p.tq ? p.T : 2 * p.tq) * p.G, turn = JOIN_WARPS * ROWS;
     const int split = FEW ? 1 : (most + turn - 1) / turn;
-    SPTS_TRY(launch_behind(paged_combine_kernel<D>, dim3(ctas - 1, p.max_groups, split), 32 * JOIN_WARPS, s, p, ctas));
+    SPTS_TRY(launch_behind(paged_combine_kernel<D, ROWS, DEEP>, dim3(ctas - 1, p.max_groups, split), 32 * JOIN_WARPS, s,
+                           p, ctas));
   }
   return SPTS_OK;
 }

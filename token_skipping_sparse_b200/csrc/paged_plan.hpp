@@ -51,9 +51,15 @@ SPTS_HD int64_t plan_cost(int base, int p, int w) {
   return static_cast<int64_t>(p) * base + static_cast<int64_t>(w) * p * (p + 1) / 2;
 }
 
+// a / b for a >= 0, b > 0, in 32 bits where they fit (a 64-bit division takes
+// the GPU several times as long).
+SPTS_HD int64_t plan_div(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
 // Range r of `nr` equal ranges of `total`.
 SPTS_HD int64_t plan_cut(int64_t total, int nr, int r) {
-  const int64_t q = total / nr, m = total % nr;
+  const int64_t q = plan_div(total, nr), m = total - q * nr;
   return q * r + (r < m ? r : m);
 }
 
@@ -97,7 +103,7 @@ SPTS_HD PlanUnit plan_locate(const PlanSeq &s, int w, int heads, int64_t y) {
   u.p = lo;
   u.c = base + (lo + 1) * w;
   const int64_t z = y - plan_cost(base, lo, w) * heads;
-  u.g = static_cast<int>(z / u.c);
+  u.g = static_cast<int>(plan_div(z, u.c));
   u.off = static_cast<int>(z - static_cast<int64_t>(u.g) * u.c);
   return u;
 }
