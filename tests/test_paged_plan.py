@@ -18,12 +18,14 @@ SHIM = r"""
 using namespace spts;
 // Walks every range of one head group as the kernel does.  rows: 9 ints per piece
 // (range, b, p, g, t0, t1, tiles, whole, slot); cuts: the record of each range.
-extern "C" int walk(int B, const int *n, const int *L, int w, int heads, int ctas, int *rows, int cap, PlanCut *cuts) {
+extern "C" int walk(int B, const int *n, const int *L, int w, int tile, int heads, int ctas, int *rows, int cap,
+                    PlanCut *cuts) {
+  const PlanShape sh{w, tile};
   std::vector<PlanSeq> seq(B);
   std::vector<int64_t> before(B + 1, 0);
   for (int b = 0; b < B; ++b) {
     seq[b] = PlanSeq{n[b], L[b]};
-    before[b + 1] = before[b] + plan_cost(plan_base(seq[b], w), plan_windows(n[b], w), w);
+    before[b + 1] = before[b] + plan_cost(plan_base(seq[b], sh), plan_windows(n[b], w), w);
   }
   const int64_t total = before[B] * heads;
   const int nr = plan_ranges(total, ctas);
@@ -31,10 +33,10 @@ extern "C" int walk(int B, const int *n, const int *L, int w, int heads, int cta
   for (int r = 0; r < nr; ++r) {
     const int64_t x = plan_cut(total, nr, r);
     PlanCursor cur;
-    plan_open(cur, seq.data(), before.data(), B, w, heads, x, plan_cut(total, nr, r + 1) - x);
+    plan_open(cur, seq.data(), before.data(), B, sh, heads, x, plan_cut(total, nr, r + 1) - x);
     cuts[r] = PlanCut{total, nr, cur.b, cur.p, cur.g, cur.off, cur.c, n[cur.b], L[cur.b], 0};
     PlanPiece pc;
-    while (plan_next(cur, seq.data(), B, w, heads, pc)) {
+    while (plan_next(cur, seq.data(), B, sh, heads, pc)) {
       if (count == cap) return -1;
       const int v[9] = {r, pc.b, pc.p, pc.g, pc.t0, pc.t1, pc.tiles, pc.whole, pc.slot};
       for (int i = 0; i < 9; ++i) rows[9 * count + i] = v[i];
@@ -67,18 +69,18 @@ def plan(tmp_path_factory):
     return C.CDLL(so)
 
 
-def run(plan, n, L, w, heads, ctas):
+def run(plan, n, L, w, heads, ctas, tile=None):
     B, cap = len(n), 200000
     rows = np.zeros((cap, 9), np.int32)
     cuts = (Cut * ctas)()
     arr = lambda v: (C.c_int * len(v))(*v)  # noqa: E731
-    count = plan.walk(B, arr(n), arr(L), w, heads, ctas, rows.ctypes.data_as(C.c_void_p), cap, cuts)
+    count = plan.walk(B, arr(n), arr(L), w, tile or -(-w // 2), heads, ctas, rows.ctypes.data_as(C.c_void_p), cap, cuts)
     assert count >= 0
     return rows[:count], cuts
 
 
-def check(plan, n, L, w, heads, ctas):
-    rows, cuts = run(plan, n, L, w, heads, ctas)
+def check(plan, n, L, w, heads, ctas, tile=None):
+    rows, cuts = run(plan, n, L, w, heads, ctas, tile)
     want = {}
     for b, (m, length) in enumerate(zip(n, L)):
         for p in range(-(-m // w)):
@@ -146,6 +148,8 @@ def test_ragged_batches(plan):
         L = [int(max(0, m + rng.integers(-3 if m else 0, rng.choice([1, 50, 4000])))) for m in n]
         w = 2 * (128 // int(rng.choice([1, 2, 3, 4, 7, 8, 32])))
         check(plan, n, L, w, int(rng.integers(1, 9)), int(rng.choice([1, 2, 7, 148])))
+        w = 16 // int(rng.choice([1, 3, 4, 16]))  # windows of one Q tile
+        check(plan, n, L, w, int(rng.integers(1, 9)), int(rng.choice([1, 2, 7, 148])), tile=w)
 
 
 def test_nothing_to_do(plan):

@@ -130,9 +130,10 @@ struct PagedAttnArgs {
   float *w_scratch;  // paged_weights_scratch(...) floats, or NULL
   float *scores;     // paged_scores_bytes(...), or NULL
 };
-// TMA maps of q (box: 64 columns x G heads x 128 / G tokens) and of the pages
-// (64 columns x one head x the rows of a page, at most 128).
-spts_status paged_maps(const PagedView &c, const PagedAttnArgs &a, CUtensorMap *q, CUtensorMap *k, CUtensorMap *v);
+// TMA maps of q (box: 64 columns x G heads x `tokens`) and of K or V pages (64
+// columns x one head x the rows of a page, at most 128).
+spts_status paged_q_map(const PagedView &c, const PagedAttnArgs &a, int tokens, CUtensorMap *q);
+spts_status paged_kv_map(const PagedView &c, const void *pages, CUtensorMap *map);
 size_t paged_attn_scratch_bytes(int B, int64_t T, int64_t slots, int Hq, int Hkv, int d);
 spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, cudaStream_t s);
 size_t paged_scores_bytes(int B, int64_t T, int64_t slots, int Hq, int Hkv);
@@ -140,8 +141,7 @@ size_t paged_scores_bytes(int B, int64_t T, int64_t slots, int Hq, int Hkv);
 // the scores that it left too, or from a second product.
 spts_status launch_stored_weights(const PagedView &c, const PagedAttnArgs &a, int64_t score_stride, cudaStream_t s);
 size_t paged_weights_scratch(int B, int64_t slots, int Hkv, int Hs);
-spts_status launch_paged_weights(const PagedView &c, const PagedAttnArgs &a, const CUtensorMap &tmQ,
-                                 const CUtensorMap &tmK, cudaStream_t s);
+spts_status launch_paged_weights(const PagedView &c, const PagedAttnArgs &a, const CUtensorMap &tmK, cudaStream_t s);
 
 struct EvictArgs {
   const float *weights;

@@ -51,7 +51,6 @@ constexpr int REG_LOW = 88, REG_HIGH = 208;
 constexpr int BKV = PLAN_TILE;
 constexpr int CHUNK = 128 * 64 * 2;   // 128 rows of 64 bf16, 128-byte swizzle
 constexpr int MAX_SEQ = 1024;
-constexpr int SLOT_ROWS = 256;        // rows of a partial result: two Q tiles
 constexpr uint32_t TMEM_COLS = 512;   // S_0 [0,128), S_1 [128,256), O_0 from 256, O_1 from 384
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 constexpr float LN2 = 0.69314718055994530942f;
@@ -62,13 +61,25 @@ constexpr float LN2 = 0.69314718055994530942f;
 // (250 rows over 32K slots: 141 us against 134).
 constexpr int POLY_EVERY = 3;
 
-template <int D>
+// Which units a launch is made for.  FULL: windows of two full Q tiles.  FEW:
+// the same, and an extra path for units of at most 16 rows (without it the
+// full units' loop is a little faster: an 8K prompt 480 us against 499).
+// STEP: windows of one Q tile of at most 16 rows; its place in shared memory
+// goes to a third stage of K and V (TODO), and one warp per S_x is the softmax.
+enum Mode { FULL, FEW, STEP };
+
+template <int D, Mode MODE>
 struct Geometry {
   static constexpr int CH = D / 64;                 // 64-column chunks of a row
   static constexpr int TILE = CH * CHUNK;           // a Q, K or V tile
-  static constexpr int STAGES = D == 128 ? 2 : 4;   // per ring: 64 KB of K and of V in flight either way
+  static constexpr int STAGES = (MODE == STEP ? 3 : 2) * (D == 128 ? 1 : 2);  // of K and of V
+  // With STEP only 16 rows of a Q tile are there; the MMA reads 128 from its
+  // place on, and the rows of S behind the first 16 are not looked at.
+  static constexpr int Q_CHUNK = MODE == STEP ? 16 * 128 : CHUNK;
+  static constexpr int Q_TILE = CH * Q_CHUNK;
+  static constexpr int WARPS = MODE == STEP ? 1 : 4;  // softmax warps per S_x
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + 2 * TILE;
+  static constexpr int OFF_K = OFF_Q + 2 * Q_TILE;
   static constexpr int OFF_V = OFF_K + STAGES * TILE;
   static constexpr int OFF_TAIL = OFF_V + STAGES * TILE;
 };
@@ -94,8 +105,8 @@ struct Tail {  // shared memory behind the tiles
   PlanSeq seq[MAX_SEQ];
   int first[MAX_SEQ];
   float2 xchg[2][2][128];  // by turns: a warpgroup without a tile may be one piece ahead
-  uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t v_raw[4];  // instead of v_full where a tile's V goes through warp 2
+  uint64_t q_full[2], q_empty[2], k_full[6], k_empty[6], v_full[6], v_empty[6];
+  uint64_t v_raw[6];  // instead of v_full where a tile's V goes through warp 2
   uint64_t s_full[2], p_ready[4], o_done[2], o_free, x_full, drain;
   uint64_t item_full[ITEMS], item_empty[ITEMS];
   Item item[ITEMS];
@@ -104,22 +115,26 @@ struct Tail {  // shared memory behind the tiles
   int groups, group_heads;  // KV heads are taken in `groups` groups of at most group_heads
 };
 
-template <int D>
+template <int D, Mode MODE>
 constexpr size_t smem_bytes() {
-  return Geometry<D>::OFF_TAIL + sizeof(Tail);
+  constexpr size_t bytes = Geometry<D, MODE>::OFF_TAIL + sizeof(Tail);
+  static_assert(bytes <= 232448, "more shared memory than a CTA can have");
+  return bytes;
 }
 
 struct Params {
   PagedView c;
   const int32_t *cu;
-  int T, Hq, G, tq;
+  int T, Hq, G;
+  int tq, w;        // tokens of a Q tile and of a window
+  int slot_rows;    // rows of a partial result: w G, rounded up
   int max_groups;   // head groups that the scratch has room for
   float scale_log2;
   __nv_bfloat16 *o;
   int64_t o_stride;
   float *lse;
-  float *part_o;    // [max_groups][ctas][2][SLOT_ROWS][D]
-  float2 *part_ml;  // [max_groups][ctas][2][SLOT_ROWS]: running maximum (log2) and sum
+  float *part_o;    // [max_groups][ctas][2][slot_rows][D]
+  float2 *part_ml;  // [max_groups][ctas][2][slot_rows]: running maximum (log2) and sum
   PlanCut *cuts;    // [max_groups][ctas]
   float *scores;    // [T, Hq, score_stride] or NULL: q . k of every row and slot, for the weights
   int64_t score_stride;
@@ -182,6 +197,7 @@ __device__ __forceinline__ void tmem_st_rows16(uint32_t addr, const uint32_t (&r
       : "memory");
 }
 
+__device__ __forceinline__ PlanShape shape_of(const Params &p) { return PlanShape{p.w, p.tq}; }
 __device__ __forceinline__ int heads_of(const Tail &t, const Params &p, int group) {
   return max(min(t.group_heads, p.c.Hkv - group * t.group_heads), 0);
 }
@@ -189,7 +205,7 @@ __device__ __forceinline__ int heads_of(const Tail &t, const Params &p, int grou
 // Warp 3, one lane: the pieces of this CTA's ranges, group after group.
 __device__ __forceinline__ void walk(Tail &t, const Params &p) {
   volatile int *abort_flag = &t.abort_flag;
-  const int w = 2 * p.tq, r = blockIdx.x;
+  const int w = p.w, r = blockIdx.x;
   int count = 0;
   bool ok = true;
   auto place = [&]() -> Item * {  // the next free place of the ring
@@ -204,9 +220,9 @@ __device__ __forceinline__ void walk(Tail &t, const Params &p) {
     if (r >= nr) continue;
     const int64_t x = plan_cut(total, nr, r);
     PlanCursor cur;
-    plan_open(cur, t.seq, t.before, p.c.B, w, heads, x, plan_cut(total, nr, r + 1) - x);
+    plan_open(cur, t.seq, t.before, p.c.B, shape_of(p), heads, x, plan_cut(total, nr, r + 1) - x);
     PlanPiece pc;
-    while (ok && plan_next(cur, t.seq, p.c.B, w, heads, pc)) {
+    while (ok && plan_next(cur, t.seq, p.c.B, shape_of(p), heads, pc)) {
       const PlanSeq s = t.seq[pc.b];
       if (pc.t0 >= pc.t1 && !pc.whole) continue;  // nothing to compute, nothing to write
       Item *it = place();
@@ -218,7 +234,7 @@ __device__ __forceinline__ void walk(Tail &t, const Params &p) {
       it->first = t.first[pc.b];
       it->tok0 = pc.p * w;
       it->g = group * t.group_heads + pc.g;
-      it->two = s.n - pc.p * w > p.tq;
+      it->two = w > p.tq && s.n - pc.p * w > p.tq;
       it->t0 = pc.t0;
       it->t1 = pc.t1;
       it->a_end = (plan_visible(s, pc.p * w + p.tq) + BKV - 1) / BKV;
@@ -251,8 +267,8 @@ __device__ __forceinline__ void read_sequences(Tail &t, const Params &p) {
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
       const int b = b0 + lane;
       int64_t x = 0;
-      if (b < p.c.B && t.seq[b].n > 2 * p.tq) shared += t.seq[b].L;
-      if (b < p.c.B) x = plan_cost(plan_base(t.seq[b], 2 * p.tq), plan_windows(t.seq[b].n, 2 * p.tq), 2 * p.tq);
+      if (b < p.c.B && t.seq[b].n > p.w) shared += t.seq[b].L;
+      if (b < p.c.B) x = plan_cost(plan_base(t.seq[b], shape_of(p)), plan_windows(t.seq[b].n, p.w), p.w);
       int64_t incl = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -273,12 +289,12 @@ __device__ __forceinline__ void read_sequences(Tail &t, const Params &p) {
   __syncthreads();
 }
 
-template <int D, bool EXACT, bool FEW>
+template <int D, bool EXACT, Mode MODE>
 __global__ void __launch_bounds__(THREADS, 1)
     paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
-  using Gm = Geometry<D>;
-  constexpr int CH = Gm::CH, TILE = Gm::TILE, STAGES = Gm::STAGES;
+  using Gm = Geometry<D, MODE>;
+  constexpr int CH = Gm::CH, TILE = Gm::TILE, STAGES = Gm::STAGES, WARPS = Gm::WARPS;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sQ = smem + Gm::OFF_Q, *sK = smem + Gm::OFF_K, *sV = smem + Gm::OFF_V;
   Tail &t = *reinterpret_cast<Tail *>(smem + Gm::OFF_TAIL);
@@ -295,8 +311,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&t.q_full[x], 1);
       mbar_init(&t.q_empty[x], 1);
       mbar_init(&t.s_full[x], 1);
-      mbar_init(&t.p_ready[2 * x], 4);  // here and below: one arrival per warp
-      mbar_init(&t.p_ready[2 * x + 1], 4);
+      mbar_init(&t.p_ready[2 * x], WARPS);  // here and below: one arrival per warp
+      mbar_init(&t.p_ready[2 * x + 1], WARPS);
       mbar_init(&t.o_done[x], 1);
     }
     for (int s = 0; s < STAGES; ++s) {
@@ -306,11 +322,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&t.v_empty[s], 1);
       mbar_init(&t.v_raw[s], 1);
     }
-    mbar_init(&t.o_free, 8);
-    mbar_init(&t.x_full, 8);
+    mbar_init(&t.o_free, 2 * WARPS);
+    mbar_init(&t.x_full, 2 * WARPS);
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(&t.item_full[i], 1);
-      mbar_init(&t.item_empty[i], 11);  // a lane of every other warp
+      mbar_init(&t.item_empty[i], 3 + 2 * WARPS);  // warps 0 to 2 and the softmax
     }
     mbar_init(&t.drain, 1);
     t.abort_flag = 0;
@@ -384,7 +400,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (lane == 0) {
             mbar_arrive_expect_tx(&t.q_full[qs], p.tq * p.G * D * 2);
             for (int e = 0; e < CH; ++e)
-              tma_load_3d(sQ + qs * TILE + e * CHUNK, &tmQ, &t.q_full[qs], e * 64, g * p.G, row0 + x * p.tq);
+              tma_load_3d(sQ + qs * Gm::Q_TILE + e * Gm::Q_CHUNK, &tmQ, &t.q_full[qs], e * 64, g * p.G, row0 + x * p.tq);
           }
           q_issued |= 1u << qs;
           q_par = (q_par & ~(1u << qs)) | (qph << qs);
@@ -432,10 +448,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!wait_all(&t.q_full[qs], (q >> 1) & 1, 0x54u)) return false;
       if (!wait_all(&t.k_full[st], (k / STAGES) & 1, 0x55u)) return false;
       tc_fence_after();
-      const uint32_t k_addr = smem_u32(sK + st * TILE), q_addr = smem_u32(sQ + qs * TILE);
+      const uint32_t k_addr = smem_u32(sK + st * TILE), q_addr = smem_u32(sQ + qs * Gm::Q_TILE);
 #pragma unroll
       for (int kk = 0; kk < 4 * CH; ++kk) {
-        const uint64_t a = sdesc_k_sw128(q_addr + (kk >> 2) * CHUNK) + 2 * (kk & 3);
+        const uint64_t a = sdesc_k_sw128(q_addr + (kk >> 2) * Gm::Q_CHUNK) + 2 * (kk & 3);
         const uint64_t b = sdesc_k_sw128(k_addr + (kk >> 2) * CHUNK) + 2 * (kk & 3);
         mma_bf16_ss_w(tmem + x * BKV, a, b, idesc_s, kk > 0);
       }
@@ -465,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Item *it = take(item);
       if (!it) break;
       const int t0 = uniform(it->t0), n = uniform(it->t1) - t0;
-      const bool two = uniform(it->two) != 0;
+      const bool two = MODE != STEP && uniform(it->two) != 0;
       // tiles of x = 0 when it has a Q tile of its own
       const int n_a = max(min(uniform(it->a_end) - t0, n), 0);
       give_back(item);
@@ -578,7 +594,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // every tile, a quarter of their columns each.
     const int na = (lane >> 2) / p.G, nb = ((lane >> 2) + 8) / p.G;  // their tokens
     uint32_t used = 0, joins = 0;  // tiles processed, exchanges with the other warpgroup
-    bool ok = true;
+    bool ok = quad < WARPS;
     for (int item = 0; ok; ++item) {
       const Item *it = take(item);
       if (!it) break;
@@ -588,7 +604,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       {
         const PlanSeq s{it->n, it->L};
         const int tok0 = it->tok0;
-        two = it->two != 0;
+        two = MODE != STEP && it->two != 0;
         const int shift = two ? x * p.tq : 0;  // this tile's first token in the window
         live = rt < p.tq && tok0 + shift + rt < s.n;
         lim = live ? plan_visible(s, tok0 + shift + rt + 1) : 0;
@@ -606,7 +622,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       const bool any_live = __any_sync(0xffffffffu, live);
-      const bool few = FEW && !two && (it->n - it->tok0) * p.G <= 16;
+      const bool few = MODE == STEP || (MODE == FEW && !two && (it->n - it->tok0) * p.G <= 16);
       float m_run = -INFINITY, l = 0.f;
       int j0 = (t0 + (step == 2 ? x : 0)) * BKV;
       if (few && quad == 0) {
@@ -615,7 +631,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // row over 128K slots: 102.4 us against 103.6, with pages of 16 slots
         // 115 against 132).
         const PlanSeq s{it->n, it->L};
-        const int tok0 = it->tok0, left = s.n - tok0;
+        const int tok0 = it->tok0, left = min(s.n - tok0, p.tq);
         const int lim_a = na < left ? plan_visible(s, tok0 + na + 1) : 0;
         const int lim_b = nb < left ? plan_visible(s, tok0 + nb + 1) : 0;
         float m2[2] = {-INFINITY, -INFINITY}, l2[2] = {0.f, 0.f};
@@ -721,7 +737,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             l = lr;
           }
         }
-      } else for (int i = 0; i < own_tiles; ++i, j0 += step * BKV) {
+      } else if (MODE != STEP) for (int i = 0; i < own_tiles; ++i, j0 += step * BKV) {
         const uint32_t u = used + i;
         ok = __all_sync(0xffffffffu, mbar_wait(&t.s_full[x], u & 1, abort_flag, p.status, p.wait_ns, 0x5Bu));
         if (!ok) break;
@@ -737,7 +753,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int c = 0; c < 4; ++c)
           tmem_ld32(lane_base + s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(xr + 32 * c));
         tmem_ld_wait();
-        if (FEW && EXACT && p.scores && live) {
+        if (MODE == FEW && EXACT && p.scores && live) {
           uint4 *to = reinterpret_cast<uint4 *>(
               p.scores + (static_cast<int64_t>(it->first + it->tok0 + (two ? x * p.tq : 0) + rt) * p.Hq + it->g * p.G + rh) *
                              p.score_stride + j0);
@@ -856,7 +872,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (whole) {
           if (p.lse) p.lse[static_cast<int64_t>(tok) * p.Hq + head] = (m_run + log2f(l)) * LN2;
         } else if (any_tile) {
-          p.part_ml[part * SLOT_ROWS + row * p.G + rh] = make_float2(m_run, l);
+          p.part_ml[part * p.slot_rows + row * p.G + rh] = make_float2(m_run, l);
         }
       }
       const float inv = whole ? (lim == 0 ? 0.f : 1.f / l) : 1.f;
@@ -896,7 +912,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               dst[q] = make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
                                   pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
           } else {
-            float *dst = p.part_o + (part * SLOT_ROWS + row * p.G + rh) * D + c * 32;
+            float *dst = p.part_o + (part * p.slot_rows + row * p.G + rh) * D + c * 32;
 #pragma unroll
             for (int q = 0; q < 4; ++q) store_8(dst + 8 * q, v + 8 * q);
           }
@@ -916,7 +932,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int nr = plan_ranges(cut.total, gridDim.x);
     if (rg < nr && cut.total > 0) {
       PlanCursor cur;
-      plan_open(cur, t.seq, t.before, p.c.B, 2 * p.tq, heads, plan_cut(cut.total, nr, rg), 1);
+      plan_open(cur, t.seq, t.before, p.c.B, shape_of(p), heads, plan_cut(cut.total, nr, rg), 1);
       const PlanSeq s = t.seq[cur.b];
       cut = PlanCut{cut.total, nr,    cur.b, cur.p, group * t.group_heads + cur.g, cur.off, cur.c, s.n, s.L,
                     t.first[cur.b]};
@@ -948,7 +964,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __
   const PlanCut cut = p.cuts[group * ctas + range];
   if (!plan_first_cut(cut, range)) return;
   const PlanSeq s{cut.n, cut.L};
-  const int w = 2 * p.tq, tok0 = cut.p * w, g = cut.g;
+  const int w = p.w, tok0 = cut.p * w, g = cut.g;
   const int rows = min(w, s.n - tok0) * p.G;
   const int tiles = (plan_visible(s, tok0 + w) + BKV - 1) / BKV;
   const int lane = threadIdx.x & 31;
@@ -959,7 +975,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_combine_kernel(const __
     last = end == cut.c;
     if (off == cut.c) return -1;
     plan_tiles(off, end, cut.c, tiles, t0, t1);
-    return t0 < t1 ? ((static_cast<int64_t>(group) * ctas + rg) * 2 + slot) * SLOT_ROWS : -1;
+    return t0 < t1 ? ((static_cast<int64_t>(group) * ctas + rg) * 2 + slot) * p.slot_rows : -1;
   };
   const int warps = static_cast<int>(gridDim.z) * JOIN_WARPS;
   for (int row0 = blockIdx.z * JOIN_WARPS + (threadIdx.x >> 5); row0 < rows; row0 += warps * ROWS) {
@@ -1052,9 +1068,9 @@ struct Scratch {
   size_t bytes;
 };
 
-Scratch carve(void *base, int d, int groups, int ctas) {
+Scratch carve(void *base, int d, int groups, int ctas, int slot_rows) {
   char *at = static_cast<char *>(base);
-  const size_t slots = static_cast<size_t>(groups) * ctas * 2 * SLOT_ROWS;
+  const size_t slots = static_cast<size_t>(groups) * ctas * 2 * slot_rows;
   Scratch s;
   s.part_o = reinterpret_cast<float *>(at);
   size_t off = Carver::round(slots * d * sizeof(float));
@@ -1067,18 +1083,18 @@ Scratch carve(void *base, int d, int groups, int ctas) {
 }
 
 
-template <int D, bool EXACT, bool FEW>
+template <int D, bool EXACT, Mode MODE>
 spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const Params &p, int ctas,
                    cudaStream_t s) {
-  SPTS_TRY((allow_smem<paged_attn_kernel<D, EXACT, FEW>>(smem_bytes<D>())));
-  paged_attn_kernel<D, EXACT, FEW><<<ctas, THREADS, smem_bytes<D>(), s>>>(tq, tk, tv, p);
+  SPTS_TRY((allow_smem<paged_attn_kernel<D, EXACT, MODE>>(smem_bytes<D, MODE>())));
+  paged_attn_kernel<D, EXACT, MODE><<<ctas, THREADS, smem_bytes<D, MODE>(), s>>>(tq, tk, tv, p);
   note_launch();
   SPTS_CUDA_TRY(cudaGetLastError());
   if (ctas > 1) {
     // CTAs per unit: one turn of its warps for the largest window
-    constexpr int ROWS = FEW ? 1 : 4, DEEP = FEW ? 8 : 2;
-    const int most = (p.T < 2 * p.tq ? p.T : 2 * p.tq) * p.G, turn = JOIN_WARPS * ROWS;
-    const int split = FEW ? 1 : (most + turn - 1) / turn;
+    constexpr int ROWS = MODE == FULL ? 4 : 1, DEEP = MODE == FULL ? 2 : 8;
+    const int most = (p.T < p.w ? p.T : p.w) * p.G, turn = JOIN_WARPS * ROWS;
+    const int split = MODE == FULL ? (most + turn - 1) / turn : 1;
     SPTS_TRY(launch_behind(paged_combine_kernel<D, ROWS, DEEP>, dim3(ctas - 1, p.max_groups, split), 32 * JOIN_WARPS, s,
                            p, ctas));
   }
@@ -1087,25 +1103,51 @@ spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
 
 }  // namespace
 
-spts_status paged_maps(const PagedView &c, const PagedAttnArgs &a, CUtensorMap *q, CUtensorMap *k, CUtensorMap *v) {
-  const uint64_t D = c.d, G = a.Hq / c.Hkv, page = uint64_t(1) << c.page_shift;
-  const uint64_t q_dims[3] = {D, static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.T)};
-  const uint64_t q_strides[2] = {D * 2, static_cast<uint64_t>(a.q_stride) * 2};
-  const uint32_t q_box[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(128 / G)};
-  SPTS_TRY(make_tmap(q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, q_dims, q_strides, q_box,
-                     CU_TENSOR_MAP_SWIZZLE_128B));
+spts_status paged_q_map(const PagedView &c, const PagedAttnArgs &a, int tokens, CUtensorMap *q) {
+  const uint64_t D = c.d, G = a.Hq / c.Hkv;
+  const uint64_t dims[3] = {D, static_cast<uint64_t>(a.Hq), static_cast<uint64_t>(a.T)};
+  const uint64_t strides[2] = {D * 2, static_cast<uint64_t>(a.q_stride) * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(tokens)};
+  return make_tmap(q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+spts_status paged_kv_map(const PagedView &c, const void *pages, CUtensorMap *map) {
+  const uint64_t D = c.d, page = uint64_t(1) << c.page_shift;
   const uint64_t dims[4] = {D, static_cast<uint64_t>(c.Hkv), page, static_cast<uint64_t>(c.num_pages)};
   const uint64_t strides[3] = {D * 2, static_cast<uint64_t>(c.Hkv) * D * 2, static_cast<uint64_t>(c.page_stride) * 2};
   const uint32_t box[4] = {64, 1, static_cast<uint32_t>(page < PLAN_TILE ? page : PLAN_TILE), 1};
-  SPTS_TRY(make_tmap(k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.k, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B));
-  return make_tmap(v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.v, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  return make_tmap(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pages, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Whether the sequences have 16 rows of a KV head or less on average: then
-// the kernel with the extra path for such units.  (Without it the full
-// units' loop is a little faster: an 8K prompt 480 us against 499.)
-static bool few_rows(int B, int64_t T, int G) { return T * G <= 16 * static_cast<int64_t>(B); }
-static int64_t score_stride(int64_t slots) { return (slots + BKV - 1) / BKV * BKV; }
+namespace {
+
+// How a call is launched, from the sizes that the host knows.
+struct Shape {
+  Mode mode;
+  int tq, w;      // tokens of a Q tile and of a window
+  int groups;     // head groups that the sizes can call for (up to MAX_GROUPS: 40 MB of scratch each)
+  int slot_rows;  // rows of a partial result
+};
+constexpr int MAX_GROUPS = 4;
+
+// 16 rows of a KV head or less per sequence on average.
+bool few_rows(int B, int64_t T, int G) { return T * G <= 16 * static_cast<int64_t>(B); }
+
+Shape shape_of(int B, int64_t T, int64_t slots, int Hq, int Hkv, int d, int ctas) {
+  const int G = Hq / Hkv;
+  // One token per sequence or less on average: steps of decoding.  (Sequences
+  // with many tokens come out right, in windows of few.)
+  if (T <= B && G <= 16) return Shape{STEP, 16 / G, 16 / G, 1, 16};
+  const int tq = 128 / G, w = 2 * tq;
+  const int64_t windows = T / w + B;
+  const int groups = plan_groups(static_cast<int64_t>(B) * slots * Hkv * d * 4, windows * (slots + PLAN_TWO) * Hkv,
+                                 ctas, Hkv, MAX_GROUPS);
+  return Shape{few_rows(B, T, G) ? FEW : FULL, tq, w, groups, 256};
+}
+
+int64_t score_stride(int64_t slots) { return (slots + BKV - 1) / BKV * BKV; }
+
+}  // namespace
 
 // With few rows the attention leaves its scores (G fp32 values per slot and
 // KV head, against d bf16 values of K for computing them again), as long as
@@ -1116,36 +1158,32 @@ size_t paged_scores_bytes(int B, int64_t T, int64_t slots, int Hq, int Hkv) {
   return few_rows(B, T, Hq / Hkv) && bytes <= SCORE_BYTES ? bytes : 0;
 }
 
-// Head groups that the sizes known on the host can call for (up to MAX_GROUPS:
-// 40 MB of scratch each).
-constexpr int MAX_GROUPS = 4;
-static int max_groups(int B, int64_t T, int64_t slots, int Hq, int Hkv, int d, int ctas) {
-  const int64_t w = 2 * (128 / (Hq / Hkv)), windows = T / w + B;
-  return plan_groups(static_cast<int64_t>(B) * slots * Hkv * d * 4, windows * (slots + PLAN_TWO) * Hkv, ctas, Hkv,
-                     MAX_GROUPS);
-}
-
 size_t paged_attn_scratch_bytes(int B, int64_t T, int64_t slots, int Hq, int Hkv, int d) {
   const int ctas = num_sms();
-  return carve(nullptr, d, max_groups(B, T, slots, Hq, Hkv, d, ctas), ctas).bytes;
+  const Shape sh = shape_of(B, T, slots, Hq, Hkv, d, ctas);
+  return carve(nullptr, d, sh.groups, ctas, sh.slot_rows).bytes;
 }
 
 spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, cudaStream_t s) {
   if (a.T == 0) return SPTS_OK;
-  const int D = c.d, G = a.Hq / c.Hkv, tq = 128 / G, ctas = num_sms();
+  const int D = c.d, ctas = num_sms();
   const int64_t slots = static_cast<int64_t>(c.max_pages) << c.page_shift;
-  CUtensorMap tq_map, tk_map, tv_map;
-  SPTS_TRY(paged_maps(c, a, &tq_map, &tk_map, &tv_map));
-  const int groups = max_groups(c.B, a.T, slots, a.Hq, c.Hkv, D, ctas);
-  const Scratch sc = carve(a.scratch, D, groups, ctas);
+  const Shape sh = shape_of(c.B, a.T, slots, a.Hq, c.Hkv, D, ctas);
+  CUtensorMap q_map, k_map, v_map;
+  SPTS_TRY(paged_q_map(c, a, sh.tq, &q_map));
+  SPTS_TRY(paged_kv_map(c, c.k, &k_map));
+  SPTS_TRY(paged_kv_map(c, c.v, &v_map));
+  const Scratch sc = carve(a.scratch, D, sh.groups, ctas, sh.slot_rows);
   Params p{};
   p.c = c;
   p.cu = a.cu;
   p.T = static_cast<int>(a.T);
   p.Hq = a.Hq;
-  p.G = G;
-  p.tq = tq;
-  p.max_groups = groups;
+  p.G = a.Hq / c.Hkv;
+  p.tq = sh.tq;
+  p.w = sh.w;
+  p.slot_rows = sh.slot_rows;
+  p.max_groups = sh.groups;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.o = static_cast<__nv_bfloat16 *>(a.o);
   p.o_stride = a.o_stride;
@@ -1155,16 +1193,18 @@ spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, c
   p.cuts = sc.cuts;
   p.status = a.status;
   p.wait_ns = wait_limit_ns();
-  const bool exact = a.lse != nullptr, few = few_rows(c.B, a.T, G);
   p.scores = a.weights && a.scores ? a.scores : nullptr;
   p.score_stride = score_stride(slots);
-  auto run = D == 64 ? (exact ? (few ? launch<64, true, true> : launch<64, true, false>)
-                              : (few ? launch<64, false, true> : launch<64, false, false>))
-                     : (exact ? (few ? launch<128, true, true> : launch<128, true, false>)
-                              : (few ? launch<128, false, true> : launch<128, false, false>));
-  SPTS_TRY(run(tq_map, tk_map, tv_map, p, ctas, s));
-  if (p.scores) return launch_stored_weights(c, a, p.score_stride, s);
-  return a.weights ? launch_paged_weights(c, a, tq_map, tk_map, s) : SPTS_OK;
+  using Launch = spts_status (*)(const CUtensorMap &, const CUtensorMap &, const CUtensorMap &, const Params &, int,
+                                 cudaStream_t);
+  static constexpr Launch launches[2][2][3] = {
+      {{launch<64, false, FULL>, launch<64, false, FEW>, launch<64, false, STEP>},
+       {launch<64, true, FULL>, launch<64, true, FEW>, launch<64, true, STEP>}},
+      {{launch<128, false, FULL>, launch<128, false, FEW>, launch<128, false, STEP>},
+       {launch<128, true, FULL>, launch<128, true, FEW>, launch<128, true, STEP>}}};
+  SPTS_TRY(launches[D == 128][a.lse != nullptr][sh.mode](q_map, k_map, v_map, p, ctas, s));
+  if (a.weights == nullptr) return SPTS_OK;
+  return p.scores ? launch_stored_weights(c, a, p.score_stride, s) : launch_paged_weights(c, a, k_map, s);
 }
 
 }  // namespace spts

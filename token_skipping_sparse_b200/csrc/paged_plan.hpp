@@ -3,7 +3,7 @@
 // the host.
 //
 // Work is counted in key slots.  A unit is a window of w new tokens of one
-// sequence (two Q tiles of w / 2 tokens) and one KV head; window p of a
+// sequence (one or two Q tiles) and one KV head; window p of a
 // sequence with n new tokens behind others costs base + (p + 1) w slots: what
 // its last token sees (a little more in the last window) and a constant for
 // what a unit costs beyond its tiles, so the cost of the first p windows has a closed form and
@@ -37,14 +37,18 @@ constexpr int PLAN_ONE = SPTS_PLAN_ONE, PLAN_TWO = SPTS_PLAN_TWO;
 SPTS_HD int plan_min(int a, int b) { return a < b ? a : b; }
 SPTS_HD int plan_max(int a, int b) { return a > b ? a : b; }
 
+struct PlanShape {
+  int w, tile;  // tokens of a window (one or two Q tiles) and of a Q tile
+};
+
 struct PlanSeq {
   int n, L;  // new tokens, cached tokens (the new ones included)
 };
 
 SPTS_HD int plan_windows(int n, int w) { return (n + w - 1) / w; }
 // What every window of a sequence costs besides its own tokens.
-SPTS_HD int plan_base(const PlanSeq &s, int w) {
-  return plan_max(s.L - s.n, 0) + (s.n > w / 2 ? PLAN_TWO : PLAN_ONE);
+SPTS_HD int plan_base(const PlanSeq &s, PlanShape sh) {
+  return plan_max(s.L - s.n, 0) + (sh.w > sh.tile && s.n > sh.tile ? PLAN_TWO : PLAN_ONE);
 }
 // Cost of the first p windows of a sequence, for one head.
 SPTS_HD int64_t plan_cost(int base, int p, int w) {
@@ -91,8 +95,8 @@ SPTS_HD int plan_ranges(int64_t total, int ctas) {
 
 
 // y: position inside the sequence's units of one head group of `heads` heads.
-SPTS_HD PlanUnit plan_locate(const PlanSeq &s, int w, int heads, int64_t y) {
-  const int base = plan_base(s, w);
+SPTS_HD PlanUnit plan_locate(const PlanSeq &s, PlanShape sh, int heads, int64_t y) {
+  const int w = sh.w, base = plan_base(s, sh);
   int lo = 0, hi = plan_windows(s.n, w) - 1;  // the window, by its first position
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -125,7 +129,7 @@ struct PlanPiece {
 
 // Stands a walk at position x of a group of `heads` heads; before[b] is the
 // cost of the sequences before b for one head (before[B]: of all).
-SPTS_HD void plan_open(PlanCursor &cur, const PlanSeq *seq, const int64_t *before, int B, int w, int heads, int64_t x,
+SPTS_HD void plan_open(PlanCursor &cur, const PlanSeq *seq, const int64_t *before, int B, PlanShape sh, int heads, int64_t x,
                        int64_t length) {
   int lo = 0, hi = B - 1;  // the last sequence that begins at or before x and has any cost
   while (lo < hi) {
@@ -136,7 +140,7 @@ SPTS_HD void plan_open(PlanCursor &cur, const PlanSeq *seq, const int64_t *befor
   cur.left = length;
   cur.b = lo;
   if (length <= 0) return;
-  const PlanUnit u = plan_locate(seq[lo], w, heads, x - before[lo] * heads);
+  const PlanUnit u = plan_locate(seq[lo], sh, heads, x - before[lo] * heads);
   cur.p = u.p;
   cur.g = u.g;
   cur.off = u.off;
@@ -144,8 +148,9 @@ SPTS_HD void plan_open(PlanCursor &cur, const PlanSeq *seq, const int64_t *befor
 }
 
 // The next piece, or 0 at the end of the range.
-SPTS_HD int plan_next(PlanCursor &cur, const PlanSeq *seq, int B, int w, int heads, PlanPiece &pc) {
+SPTS_HD int plan_next(PlanCursor &cur, const PlanSeq *seq, int B, PlanShape sh, int heads, PlanPiece &pc) {
   if (cur.left <= 0 || cur.b >= B) return 0;
+  const int w = sh.w;
   const PlanSeq s = seq[cur.b];
   const int take = static_cast<int>(cur.left < cur.c - cur.off ? cur.left : cur.c - cur.off);
   pc.b = cur.b;
@@ -168,7 +173,7 @@ SPTS_HD int plan_next(PlanCursor &cur, const PlanSeq *seq, int B, int w, int hea
         while (cur.b < B && seq[cur.b].n <= 0);
       }
     }
-    if (cur.b < B) cur.c = plan_base(seq[cur.b], w) + (cur.p + 1) * w;
+    if (cur.b < B) cur.c = plan_base(seq[cur.b], sh) + (cur.p + 1) * w;
   } else {
     cur.off += take;
   }

@@ -486,8 +486,7 @@ size_t paged_weights_scratch(int B, int64_t slots, int Hkv, int Hs) {
   return Hs == 1 && Hkv > 1 && n * sizeof(float) <= SPLIT_BYTES ? n : 0;
 }
 
-spts_status launch_paged_weights(const PagedView &c, const PagedAttnArgs &a, const CUtensorMap &tmQ,
-                                 const CUtensorMap &tmK, cudaStream_t s) {
+spts_status launch_paged_weights(const PagedView &c, const PagedAttnArgs &a, const CUtensorMap &tmK, cudaStream_t s) {
   const int64_t slots = static_cast<int64_t>(c.max_pages) << c.page_shift;
   const bool split = paged_weights_scratch(c.B, slots, c.Hkv, a.Hs) > 0;
   Params p{};
@@ -506,6 +505,8 @@ spts_status launch_paged_weights(const PagedView &c, const PagedAttnArgs &a, con
   p.add = split ? 0 : 1;
   p.status = a.status;
   p.wait_ns = wait_limit_ns();
+  CUtensorMap tmQ;
+  SPTS_TRY(paged_q_map(c, a, p.tq, &tmQ));
   SPTS_TRY((c.d == 64 ? launch<64> : launch<128>)(tmQ, tmK, p, s));
   if (!split) return SPTS_OK;
   const unsigned blocks = static_cast<unsigned>((slots + 255) / 256);
