@@ -138,19 +138,32 @@ CASES = {
 }
 
 
+def widen(c, slots=1025):
+    """A table row with room for more slots than units are dealt out whole for: the work is cut across CTAs."""
+    more = -(-slots // c.page) - c.table.shape[1]
+    if more > 0:
+        c.table = torch.cat((c.table, torch.full((len(c.lens), more), -1, dtype=I32, device="cuda")), 1)
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("name", CASES)
-def test_attention(name):
+def test_attention(name, wide):
     new, old, Hq, Hkv, d, page = CASES[name]
     c = Cache([n + o for n, o in zip(new, old)], page, Hkv, d, seed=len(name))
+    if wide:
+        widen(c)
     check_attention(c, new, Hq, Hkv, d, seed=3, lse=False)
     check_attention(c, new, Hq, Hkv, d, seed=4)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("each", [True, False])
 @pytest.mark.parametrize("name", CASES)
-def test_attention_with_weights(name, each):
+def test_attention_with_weights(name, each, wide):
     new, old, Hq, Hkv, d, page = CASES[name]
     c = Cache([n + o for n, o in zip(new, old)], page, Hkv, d, seed=len(name))
+    if wide:
+        widen(c)
     check_attention(c, new, Hq, Hkv, d, seed=5, each=each, lse=False)
 
 
@@ -159,6 +172,9 @@ def test_attention_rows_that_see_no_slot_are_zero(Hq, Hkv, d):
     # more new tokens than cached ones: the first rows of the sequence come before its first slot
     c = Cache([5, 200, 0], 16, Hkv, d, seed=8)
     check_attention(c, [9, 330, 3], Hq, Hkv, d, seed=9, each=True)
+    widen(c)
+    check_attention(c, [9, 330, 3], Hq, Hkv, d, seed=9, each=True)
+    check_attention(c, [0, 1, 1], Hq, Hkv, d, seed=9, each=True)
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -219,9 +235,12 @@ def test_attention_long_enough_for_head_groups(each):
     assert bool(((w.double() - want_w).abs() <= bound).all())
 
 
-def test_one_sequence_does_not_reach_another():
+@pytest.mark.parametrize("wide", [False, True])
+def test_one_sequence_does_not_reach_another(wide):
     # non-finite rows of one sequence, and of its neighbour in the packed rows
     c = Cache([100, 50, 70], 16, 2, 128, seed=17)
+    if wide:
+        widen(c)
     p, r = P.slot_rows(c.rows[1], 50, 16)
     cu, q = packed([60, 20, 1], 8, 128, 18)
     clean = S.spts_paged_attention(q, *c.args(), i32(cu))
@@ -349,7 +368,8 @@ def test_bad_device_values_are_flagged_and_reach_no_other_sequence(bad):
     cu, q = packed(new, 8, 128, 28)
     want = P.paged_attention(f64(q), c.np_k, c.np_v, c.rows, lens, cu)
     S.check_device_status()
-    rows, sizes = [list(r) for r in c.rows], list(lens)
+    widen(c)
+    rows, sizes = c.table.tolist(), list(lens)
     if bad == "length":
         sizes[1] = 10 ** 9
     elif bad == "negative length":

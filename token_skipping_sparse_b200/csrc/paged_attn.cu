@@ -65,7 +65,8 @@ constexpr int POLY_EVERY = 3;
 // the same, and an extra path for units of at most 16 rows (without it the
 // full units' loop is a little faster: an 8K prompt 480 us against 499).
 // STEP: windows of one Q tile of at most 16 rows; its place in shared memory
-// goes to a third stage of K and V (TODO), and one warp per S_x is the softmax.
+// goes to a third stage of K and V, and one warp per S_x is the softmax (64
+// ragged sequences: 211 us against 224 with FEW).
 enum Mode { FULL, FEW, STEP };
 
 template <int D, Mode MODE>
@@ -128,6 +129,7 @@ struct Params {
   int T, Hq, G;
   int tq, w;        // tokens of a Q tile and of a window
   int slot_rows;    // rows of a partial result: w G, rounded up
+  int whole;        // units are dealt out whole
   int max_groups;   // head groups that the scratch has room for
   float scale_log2;
   __nv_bfloat16 *o;
@@ -202,51 +204,69 @@ __device__ __forceinline__ int heads_of(const Tail &t, const Params &p, int grou
   return max(min(t.group_heads, p.c.Hkv - group * t.group_heads), 0);
 }
 
-// Warp 3, one lane: the pieces of this CTA's ranges, group after group.
+// Warp 3, one lane: the pieces of this CTA's ranges, group after group, or
+// every gridDim.x-th unit.
 __device__ __forceinline__ void walk(Tail &t, const Params &p) {
   volatile int *abort_flag = &t.abort_flag;
   const int w = p.w, r = blockIdx.x;
   int count = 0;
-  bool ok = true;
   auto place = [&]() -> Item * {  // the next free place of the ring
     const int i = count % ITEMS;
-    ok = mbar_wait_long(&t.item_empty[i], ((count / ITEMS) & 1) ^ 1, abort_flag, p.status, p.wait_ns, 0x50u);
-    return &t.item[i];
+    const bool ok =
+        mbar_wait_long(&t.item_empty[i], ((count / ITEMS) & 1) ^ 1, abort_flag, p.status, p.wait_ns, 0x50u);
+    return ok ? &t.item[i] : nullptr;
   };
-  for (int group = 0; ok && group < t.groups; ++group) {
-    const int heads = heads_of(t, p, group);
-    const int64_t total = t.before[p.c.B] * heads;
-    const int nr = plan_ranges(total, gridDim.x);
-    if (r >= nr) continue;
-    const int64_t x = plan_cut(total, nr, r);
-    PlanCursor cur;
-    plan_open(cur, t.seq, t.before, p.c.B, shape_of(p), heads, x, plan_cut(total, nr, r + 1) - x);
-    PlanPiece pc;
-    while (ok && plan_next(cur, t.seq, p.c.B, shape_of(p), heads, pc)) {
-      const PlanSeq s = t.seq[pc.b];
-      if (pc.t0 >= pc.t1 && !pc.whole) continue;  // nothing to compute, nothing to write
-      Item *it = place();
-      if (!ok) break;
-      it->more = 1;
-      it->b = pc.b;
-      it->n = s.n;
-      it->L = s.L;
-      it->first = t.first[pc.b];
-      it->tok0 = pc.p * w;
-      it->g = group * t.group_heads + pc.g;
-      it->two = w > p.tq && s.n - pc.p * w > p.tq;
-      it->t0 = pc.t0;
-      it->t1 = pc.t1;
-      it->a_end = (plan_visible(s, pc.p * w + p.tq) + BKV - 1) / BKV;
-      it->whole = pc.whole;
-      it->part = (group * static_cast<int>(gridDim.x) + r) * 2 + pc.slot;
-      mbar_arrive(&t.item_full[count % ITEMS]);
-      ++count;
+  auto hand_out = [&](const PlanPiece &pc, int g, int part) -> bool {
+    Item *it = place();
+    if (it == nullptr) return false;
+    const PlanSeq s = t.seq[pc.b];
+    it->more = 1;
+    it->b = pc.b;
+    it->n = s.n;
+    it->L = s.L;
+    it->first = t.first[pc.b];
+    it->tok0 = pc.p * w;
+    it->g = g;
+    it->two = w > p.tq && s.n - pc.p * w > p.tq;
+    it->t0 = pc.t0;
+    it->t1 = pc.t1;
+    it->a_end = (plan_visible(s, pc.p * w + p.tq) + BKV - 1) / BKV;
+    it->whole = pc.whole;
+    it->part = part;
+    mbar_arrive(&t.item_full[count % ITEMS]);
+    ++count;
+    return true;
+  };
+  if (p.whole) {
+    PlanPiece pc{};
+    pc.whole = 1;
+    const int64_t units = t.before[p.c.B] * p.c.Hkv;
+    for (int64_t u = r; u < units; u += gridDim.x) {
+      while (t.before[pc.b + 1] * p.c.Hkv <= u) ++pc.b;
+      const int64_t i = u - t.before[pc.b] * p.c.Hkv;
+      pc.p = static_cast<int>(plan_div(i, p.c.Hkv));
+      pc.t1 = (plan_visible(t.seq[pc.b], (pc.p + 1) * w) + BKV - 1) / BKV;
+      if (!hand_out(pc, static_cast<int>(i - static_cast<int64_t>(pc.p) * p.c.Hkv), 0)) return;
+    }
+  } else {
+    for (int group = 0; group < t.groups; ++group) {
+      const int heads = heads_of(t, p, group);
+      const int64_t total = t.before[p.c.B] * heads;
+      const int nr = plan_ranges(total, gridDim.x);
+      if (r >= nr) continue;
+      const int64_t x = plan_cut(total, nr, r);
+      PlanCursor cur;
+      plan_open(cur, t.seq, t.before, p.c.B, shape_of(p), heads, x, plan_cut(total, nr, r + 1) - x);
+      PlanPiece pc;
+      while (plan_next(cur, t.seq, p.c.B, shape_of(p), heads, pc)) {
+        if (pc.t0 >= pc.t1 && !pc.whole) continue;  // nothing to compute, nothing to write
+        if (!hand_out(pc, group * t.group_heads + pc.g, (group * static_cast<int>(gridDim.x) + r) * 2 + pc.slot))
+          return;
+      }
     }
   }
-  if (!ok) return;
   Item *it = place();
-  if (!ok) return;
+  if (it == nullptr) return;
   it->more = 0;
   mbar_arrive(&t.item_full[count % ITEMS]);
 }
@@ -268,7 +288,8 @@ __device__ __forceinline__ void read_sequences(Tail &t, const Params &p) {
       const int b = b0 + lane;
       int64_t x = 0;
       if (b < p.c.B && t.seq[b].n > p.w) shared += t.seq[b].L;
-      if (b < p.c.B) x = plan_cost(plan_base(t.seq[b], shape_of(p)), plan_windows(t.seq[b].n, p.w), p.w);
+      if (b < p.c.B && p.whole) x = plan_windows(t.seq[b].n, p.w);
+      else if (b < p.c.B) x = plan_cost(plan_base(t.seq[b], shape_of(p)), plan_windows(t.seq[b].n, p.w), p.w);
       int64_t incl = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -925,7 +946,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
   // what this CTA's ranges leave for the combine kernel
-  if (threadIdx.x < p.max_groups) {
+  if (threadIdx.x < p.max_groups && !p.whole) {
     const int group = threadIdx.x, heads = group < t.groups ? heads_of(t, p, group) : 0, rg = blockIdx.x;
     PlanCut cut{};
     cut.total = heads > 0 ? t.before[p.c.B] * heads : 0;
@@ -1090,7 +1111,7 @@ spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   paged_attn_kernel<D, EXACT, MODE><<<ctas, THREADS, smem_bytes<D, MODE>(), s>>>(tq, tk, tv, p);
   note_launch();
   SPTS_CUDA_TRY(cudaGetLastError());
-  if (ctas > 1) {
+  if (ctas > 1 && !p.whole) {
     // CTAs per unit: one turn of its warps for the largest window
     constexpr int ROWS = MODE == FULL ? 4 : 1, DEEP = MODE == FULL ? 2 : 8;
     const int most = (p.T < p.w ? p.T : p.w) * p.G, turn = JOIN_WARPS * ROWS;
@@ -1124,25 +1145,30 @@ namespace {
 // How a call is launched, from the sizes that the host knows.
 struct Shape {
   Mode mode;
+  int whole;      // units are dealt out whole: no scratch, no combine kernel
   int tq, w;      // tokens of a Q tile and of a window
   int groups;     // head groups that the sizes can call for (up to MAX_GROUPS: 40 MB of scratch each)
   int slot_rows;  // rows of a partial result
 };
 constexpr int MAX_GROUPS = 4;
+constexpr int64_t WHOLE_SLOTS = 1024;
 
 // 16 rows of a KV head or less per sequence on average.
 bool few_rows(int B, int64_t T, int G) { return T * G <= 16 * static_cast<int64_t>(B); }
 
 Shape shape_of(int B, int64_t T, int64_t slots, int Hq, int Hkv, int d, int ctas) {
   const int G = Hq / Hkv;
+  // Up to WHOLE_SLOTS slots a unit takes no longer than joining its pieces
+  // would (one row over 517 slots: 10.3 us on the GPU against 13.9).
+  const int whole = slots <= WHOLE_SLOTS;
   // One token per sequence or less on average: steps of decoding.  (Sequences
   // with many tokens come out right, in windows of few.)
-  if (T <= B && G <= 16) return Shape{STEP, 16 / G, 16 / G, 1, 16};
+  if (T <= B && G <= 16) return Shape{STEP, whole, 16 / G, 16 / G, whole ? 0 : 1, 16};
   const int tq = 128 / G, w = 2 * tq;
   const int64_t windows = T / w + B;
   const int groups = plan_groups(static_cast<int64_t>(B) * slots * Hkv * d * 4, windows * (slots + PLAN_TWO) * Hkv,
                                  ctas, Hkv, MAX_GROUPS);
-  return Shape{few_rows(B, T, G) ? FEW : FULL, tq, w, groups, 256};
+  return Shape{few_rows(B, T, G) ? FEW : FULL, whole, tq, w, whole ? 0 : groups, 256};
 }
 
 int64_t score_stride(int64_t slots) { return (slots + BKV - 1) / BKV * BKV; }
@@ -1183,6 +1209,7 @@ spts_status launch_paged_attention(const PagedView &c, const PagedAttnArgs &a, c
   p.tq = sh.tq;
   p.w = sh.w;
   p.slot_rows = sh.slot_rows;
+  p.whole = sh.whole;
   p.max_groups = sh.groups;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.o = static_cast<__nv_bfloat16 *>(a.o);
