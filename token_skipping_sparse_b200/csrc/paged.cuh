@@ -93,13 +93,15 @@ spts_status allow_smem(size_t bytes) {
 // Launches a kernel that may start while the one before it on the stream still
 // runs, and waits for it itself (griddepcontrol.wait).
 template <typename... Want, typename... Args>
-spts_status launch_behind(void (*kernel)(Want...), dim3 grid, int threads, cudaStream_t s, Args &&...args) {
+spts_status launch_behind(void (*kernel)(Want...), dim3 grid, int threads, cudaStream_t s, size_t smem,
+                          Args &&...args) {
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &early;
   cfg.numAttrs = 1;

@@ -1117,7 +1117,7 @@ spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
     const int most = (p.T < p.w ? p.T : p.w) * p.G, turn = JOIN_WARPS * ROWS;
     const int split = MODE == FULL ? (most + turn - 1) / turn : 1;
     SPTS_TRY(launch_behind(paged_combine_kernel<D, ROWS, DEEP>, dim3(ctas - 1, p.max_groups, split), 32 * JOIN_WARPS, s,
-                           p, ctas));
+                           0, p, ctas));
   }
   return SPTS_OK;
 }

@@ -454,14 +454,14 @@ spts_status launch_cache_evict(const PagedView &c, const EvictArgs &e, cudaStrea
   SPTS_CUDA_TRY(cudaLaunchKernelEx(&cfg, evict_select_kernel, c, e, ctas, max_keys));
   note_launch();
   if (e.dst_table == c.table) {
-    SPTS_TRY(launch_behind(evict_shift_kernel, dim3(static_cast<unsigned>(units * 2 * (c.d / 32))), SHIFT_THREADS, s, c,
-                           e));
+    SPTS_TRY(launch_behind(evict_shift_kernel, dim3(static_cast<unsigned>(units * 2 * (c.d / 32))), SHIFT_THREADS, s, 0,
+                           c, e));
     evict_weights_kernel<<<rows, MOVE_THREADS, 0, s>>>(c, e);
     note_launch();
     SPTS_CUDA_TRY(cudaGetLastError());
     return SPTS_OK;
   }
-  return launch_behind(evict_copy_kernel, dim3(static_cast<unsigned>(units * (parts + 1))), MOVE_THREADS, s, c, e,
+  return launch_behind(evict_copy_kernel, dim3(static_cast<unsigned>(units * (parts + 1))), MOVE_THREADS, s, 0, c, e,
                        parts);
 }
 
