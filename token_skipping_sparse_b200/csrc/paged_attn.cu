@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (lane == 0) {
             mbar_arrive_expect_tx(&t.q_full[qs], p.tq * p.G * D * 2);
             for (int e = 0; e < CH; ++e)
-              tma_load_3d(sQ + qs * Gm::Q_TILE + e * Gm::Q_CHUNK, &tmQ, &t.q_full[qs], e * 64, g * p.G, row0 + x * p.tq);
+              tma_load_3d(sQ + qs * Gm::Q_TILE + e * Gm::Q_CHUNK, &tmQ, &t.q_full[qs], e * 64, g * p.G,
+                          row0 + x * p.tq);
           }
           q_issued |= 1u << qs;
           q_par = (q_par & ~(1u << qs)) | (qph << qs);
@@ -667,7 +668,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_ld_wait();
           if (EXACT && p.scores) {
             // the rows' scores as they are: a slot past a row's limit is not read again
-            const int64_t row = (static_cast<int64_t>(it->first + tok0) * p.Hq + it->g * p.G) * p.score_stride + j0 + my;
+            const int64_t row =
+                (static_cast<int64_t>(it->first + tok0) * p.Hq + it->g * p.G) * p.score_stride + j0 + my;
             const int64_t row_a = row + (static_cast<int64_t>(na) * p.Hq + (lane >> 2) - na * p.G) * p.score_stride;
             const int64_t row_b = row + (static_cast<int64_t>(nb) * p.Hq + (lane >> 2) + 8 - nb * p.G) * p.score_stride;
 #pragma unroll
@@ -758,95 +760,96 @@ __global__ void __launch_bounds__(THREADS, 1)
             l = lr;
           }
         }
-      } else if (MODE != STEP) for (int i = 0; i < own_tiles; ++i, j0 += step * BKV) {
-        const uint32_t u = used + i;
-        ok = __all_sync(0xffffffffu, mbar_wait(&t.s_full[x], u & 1, abort_flag, p.status, p.wait_ns, 0x5Bu));
-        if (!ok) break;
-        if (!any_live) {  // a warp of padding rows: P may be anything
-          tc_fence_before();
-          mbar_arrive_warp(&t.p_ready[2 * x]);
-          mbar_arrive_warp(&t.p_ready[2 * x + 1]);
-          continue;
-        }
-        tc_fence_after();
-        uint32_t xr[BKV];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          tmem_ld32(lane_base + s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(xr + 32 * c));
-        tmem_ld_wait();
-        if (MODE == FEW && EXACT && p.scores && live) {
-          uint4 *to = reinterpret_cast<uint4 *>(
-              p.scores + (static_cast<int64_t>(it->first + it->tok0 + (two ? x * p.tq : 0) + rt) * p.Hq + it->g * p.G + rh) *
-                             p.score_stride + j0);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) to[e] = make_uint4(xr[4 * e], xr[4 * e + 1], xr[4 * e + 2], xr[4 * e + 3]);
-        }
-        if (j0 + BKV > mask_from) {  // slots past the tile's first query, past the last slot among them
-          const int vis = lim - j0;
-#pragma unroll
-          for (int c = 0; c < BKV; ++c)
-            if (c >= vis) xr[c] = 0xff800000u;  // -inf
-        }
-        float m8[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m8[e] = __uint_as_float(xr[e]);
-#pragma unroll
-        for (int c = 8; c < BKV; c += 2)
-          m8[(c >> 1) & 7] = max3_nan(m8[(c >> 1) & 7], __uint_as_float(xr[c]), __uint_as_float(xr[c + 1]));
-        const float mt = max3_nan(max3_nan(m8[0], m8[1], m8[2]), max3_nan(m8[3], m8[4], m8[5]),
-                                  max_nan(m8[6], m8[7])) * c2;
-        const float m_new = max_nan(m_run, mt);
-        const bool need = live && !(m_new <= m_run + RESCALE_THRESHOLD);
-        if (__any_sync(0xffffffffu, need)) {
-          const float factor = (m_run == -INFINITY) ? 0.f : ex2(m_run - m_new);
-          if (i > 0) {  // O_x holds the tiles so far: wait for the last of them
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait(&t.o_done[x], (u - 1) & 1, abort_flag, p.status, p.wait_ns, 0x5Cu));
-            if (!ok) break;
-            tc_fence_after();
-            rescale_o(factor);
-          }
-          l *= factor;
-          m_run = m_new;
-        }
-        const float neg_m = (m_run == -INFINITY) ? 0.f : -m_run;
-        const uint64_t cc = f2pack(c2, c2), mm = f2pack(neg_m, neg_m);
-        uint64_t s4[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const uint64_t a2 =
-                f2fma(f2pack(__uint_as_float(xr[h * 64 + 2 * e]), __uint_as_float(xr[h * 64 + 2 * e + 1])), cc, mm);
-            float e0, e1;
-            if (!EXACT && e % POLY_EVERY == POLY_EVERY - 1) {
-              exp2_poly2(a2, e0, e1);
-            } else {
-              float a0, a1;
-              f2unpack(a2, a0, a1);
-              e0 = ex2(a0);
-              e1 = ex2(a1);
-            }
-            s4[e & 3] = f2add(s4[e & 3], f2pack(e0, e1));
-            pk[e] = pack_bf16x2(e0, e1);
-          }
-          tmem_st32(lane_base + s_col + h * 32, pk);  // P over S: columns [32 h, 32 h + 32)
-          if (h == 0) {
-            tmem_st_wait();
+      } else if (MODE != STEP) {
+        for (int i = 0; i < own_tiles; ++i, j0 += step * BKV) {
+          const uint32_t u = used + i;
+          ok = __all_sync(0xffffffffu, mbar_wait(&t.s_full[x], u & 1, abort_flag, p.status, p.wait_ns, 0x5Bu));
+          if (!ok) break;
+          if (!any_live) {  // a warp of padding rows: P may be anything
             tc_fence_before();
             mbar_arrive_warp(&t.p_ready[2 * x]);
+            mbar_arrive_warp(&t.p_ready[2 * x + 1]);
+            continue;
           }
+          tc_fence_after();
+          uint32_t xr[BKV];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            tmem_ld32(lane_base + s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(xr + 32 * c));
+          tmem_ld_wait();
+          if (MODE == FEW && EXACT && p.scores && live) {
+            const int64_t row = static_cast<int64_t>(it->first + it->tok0 + (two ? x * p.tq : 0) + rt) * p.Hq;
+            uint4 *to = reinterpret_cast<uint4 *>(p.scores + (row + it->g * p.G + rh) * p.score_stride + j0);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) to[e] = make_uint4(xr[4 * e], xr[4 * e + 1], xr[4 * e + 2], xr[4 * e + 3]);
+          }
+          if (j0 + BKV > mask_from) {  // slots past the tile's first query, past the last slot among them
+            const int vis = lim - j0;
+#pragma unroll
+            for (int c = 0; c < BKV; ++c)
+              if (c >= vis) xr[c] = 0xff800000u;  // -inf
+          }
+          float m8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m8[e] = __uint_as_float(xr[e]);
+#pragma unroll
+          for (int c = 8; c < BKV; c += 2)
+            m8[(c >> 1) & 7] = max3_nan(m8[(c >> 1) & 7], __uint_as_float(xr[c]), __uint_as_float(xr[c + 1]));
+          const float mt = max3_nan(max3_nan(m8[0], m8[1], m8[2]), max3_nan(m8[3], m8[4], m8[5]),
+                                    max_nan(m8[6], m8[7])) * c2;
+          const float m_new = max_nan(m_run, mt);
+          const bool need = live && !(m_new <= m_run + RESCALE_THRESHOLD);
+          if (__any_sync(0xffffffffu, need)) {
+            const float factor = (m_run == -INFINITY) ? 0.f : ex2(m_run - m_new);
+            if (i > 0) {  // O_x holds the tiles so far: wait for the last of them
+              ok = __all_sync(0xffffffffu,
+                              mbar_wait(&t.o_done[x], (u - 1) & 1, abort_flag, p.status, p.wait_ns, 0x5Cu));
+              if (!ok) break;
+              tc_fence_after();
+              rescale_o(factor);
+            }
+            l *= factor;
+            m_run = m_new;
+          }
+          const float neg_m = (m_run == -INFINITY) ? 0.f : -m_run;
+          const uint64_t cc = f2pack(c2, c2), mm = f2pack(neg_m, neg_m);
+          uint64_t s4[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const uint64_t a2 =
+                  f2fma(f2pack(__uint_as_float(xr[h * 64 + 2 * e]), __uint_as_float(xr[h * 64 + 2 * e + 1])), cc, mm);
+              float e0, e1;
+              if (!EXACT && e % POLY_EVERY == POLY_EVERY - 1) {
+                exp2_poly2(a2, e0, e1);
+              } else {
+                float a0, a1;
+                f2unpack(a2, a0, a1);
+                e0 = ex2(a0);
+                e1 = ex2(a1);
+              }
+              s4[e & 3] = f2add(s4[e & 3], f2pack(e0, e1));
+              pk[e] = pack_bf16x2(e0, e1);
+            }
+            tmem_st32(lane_base + s_col + h * 32, pk);  // P over S: columns [32 h, 32 h + 32)
+            if (h == 0) {
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive_warp(&t.p_ready[2 * x]);
+            }
+          }
+          {
+            float q0, q1, q2, q3;
+            f2unpack(f2add(s4[0], s4[1]), q0, q1);
+            f2unpack(f2add(s4[2], s4[3]), q2, q3);
+            l += (q0 + q1) + (q2 + q3);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive_warp(&t.p_ready[2 * x + 1]);
         }
-        {
-          float q0, q1, q2, q3;
-          f2unpack(f2add(s4[0], s4[1]), q0, q1);
-          f2unpack(f2add(s4[2], s4[3]), q2, q3);
-          l += (q0 + q1) + (q2 + q3);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive_warp(&t.p_ready[2 * x + 1]);
       }
       if (!ok) break;
       used += own_tiles;

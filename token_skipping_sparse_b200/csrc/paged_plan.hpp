@@ -129,8 +129,8 @@ struct PlanPiece {
 
 // Stands a walk at position x of a group of `heads` heads; before[b] is the
 // cost of the sequences before b for one head (before[B]: of all).
-SPTS_HD void plan_open(PlanCursor &cur, const PlanSeq *seq, const int64_t *before, int B, PlanShape sh, int heads, int64_t x,
-                       int64_t length) {
+SPTS_HD void plan_open(PlanCursor &cur, const PlanSeq *seq, const int64_t *before, int B, PlanShape sh, int heads,
+                       int64_t x, int64_t length) {
   int lo = 0, hi = B - 1;  // the last sequence that begins at or before x and has any cost
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;

@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool on = wg < un->tiles;
       const int n = un->n, L = un->L, q0 = un->q0, q1 = un->q1, g0 = un->g0, first = un->first;
       const int slot = un->slot0 + wg * BKV + r, base = L - n;
-      float *w = p.out + (static_cast<int64_t>(un->b) * p.out_heads + (p.out_heads == 1 ? 0 : g0)) * p.out_stride + slot;
+      const int64_t out_row = static_cast<int64_t>(un->b) * p.out_heads + (p.out_heads == 1 ? 0 : g0);
+      float *w = p.out + out_row * p.out_stride + slot;
       give_back(i);
       if (!on) continue;
       const float old = p.add && slot < L ? *w : 0.f;
@@ -494,8 +495,8 @@ spts_status launch(const CUtensorMap &q, const CUtensorMap &k, const Params &p, 
 
 spts_status launch_stored_weights(const PagedView &c, const PagedAttnArgs &a, int64_t score_stride, cudaStream_t s) {
   const int64_t slots = static_cast<int64_t>(c.max_pages) << c.page_shift, chunks = (slots + 127) / 128;
-  return launch_behind(stored_weights_kernel, dim3(static_cast<unsigned>(chunks * c.B * a.Hs)), 32 * STORED_WARPS, s, 0, c,
-                       a.cu,
+  const dim3 grid(static_cast<unsigned>(chunks * c.B * a.Hs));
+  return launch_behind(stored_weights_kernel, grid, 32 * STORED_WARPS, s, 0, c, a.cu,
                        static_cast<int>(a.T), a.Hq, a.scale * LOG2E, static_cast<const float *>(a.scores), score_stride,
                        static_cast<const float *>(a.lse), a.weights, a.Hs, a.w_stride, static_cast<int>(chunks));
 }
