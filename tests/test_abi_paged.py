@@ -116,3 +116,35 @@ def test_paged_cache_calls_want_cuda_tensors_of_the_right_kind():
         S._lib._paged(k, k[..., :32], torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), k.device)
     with pytest.raises(ValueError, match="per sequence"):
         S._lib._paged(k, k, torch.zeros(2, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), k.device)
+
+
+def test_paged_cache_calls_refuse_overlapping_rows():
+    """A stride of 0 (a tensor that was expanded) would read as "contiguous" behind the C interface."""
+    import pytest
+    import torch
+    import token_skipping_sparse_b200 as S
+    k, table, lens = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16), torch.zeros(3, 4, dtype=torch.int32), \
+        torch.zeros(3, dtype=torch.int32)
+    cpu = k.device
+    assert S._lib._paged(k, k, table, lens, cpu)[1:] == (2, 64, 3, 16, 4)
+    assert S._lib._paged(k[1:].expand(1, 16, 2, 64), k[:1], table[:, 1:], lens, cpu)[5] == 3
+    one = k[:1].expand(2, 16, 2, 64)
+    with pytest.raises(ValueError, match="pages must not overlap"):
+        S._lib._paged(one, one, table, lens, cpu)
+    shared = table[:1].expand(3, 4)
+    with pytest.raises(ValueError, match="per sequence"):
+        S._lib._paged(k, k, shared, lens, cpu)
+    with pytest.raises(ValueError, match="per sequence"):
+        S._lib._paged(k, k, table, lens[:1].expand(3), cpu)
+    with pytest.raises(ValueError, match="overlap"):
+        S._lib._table_stride(shared, "dst_table")
+    assert S._lib._table_stride(table[:, :2], "dst_table") == 4
+
+    class Here:
+        index = cpu.index if cpu.index is not None else -1
+    q = torch.zeros(5, 4, 64, dtype=torch.bfloat16)
+    assert S._lib._packed(q, Here, "q") == 256
+    assert S._lib._packed(torch.zeros(5, 6, 64, dtype=torch.bfloat16)[:, 1:5], Here, "q") == 384
+    for bad in (q[:1].expand(5, 4, 64), q[:, :1].expand(5, 4, 64), q.transpose(0, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            S._lib._packed(bad, Here, "q")

@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import os
+import struct
 import threading
 
 import torch
@@ -146,7 +147,10 @@ _sig("spts_schedule_forward", i32, [C.POINTER(LayerDesc), C.POINTER(LayerWeights
                                     C.POINTER(C.c_int64), i32, i64, vp, vp, i64, C.POINTER(C.c_int64), vp, i64,
                                     C.POINTER(C.c_int64), vp, sz, vp])
 _sig("spts_schedule_forward_workspace", sz, [C.POINTER(LayerDesc), i64])
-PC = C.POINTER(PagedCache)
+# a PagedCache goes by its address or as bytes laid out alike, which take a fraction of the time to make
+PC = vp
+_pack_cache = struct.Struct("@PPqqiiPiqP").pack
+assert struct.calcsize("@PPqqiiPiqP") == C.sizeof(PagedCache)
 _sig("spts_cache_append", i32, [AD, PC, vp, i64, vp, i64, vp, i64, vp, f64, vp, vp])
 _sig("spts_paged_attention", i32, [AD, PC, vp, i64, vp, i64, vp, i64, vp, vp, i32, i64, vp, sz, vp])
 _sig("spts_paged_attention_workspace", sz, [AD, PC, i64, i32])
@@ -391,6 +395,8 @@ def spts_inject_salience(k, q_probe, rows, shift):
 _BF, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None) or torch.cuda.is_current_stream_capturing
 
 
 def _want(t, dtype, dims, device, what):
@@ -403,65 +409,79 @@ def _want(t, dtype, dims, device, what):
 
 def _packed(t, dev, what):
     """Row stride of packed tokens [T, H, d] whose heads lie as in a contiguous tensor."""
-    st = t.stride()
-    if t.dtype is not _BF or len(st) != 3 or t.get_device() != dev.index:
+    shape = t.shape
+    if t.dtype is not _BF or len(shape) != 3 or t.get_device() != dev.index:
         _want(t, _BF, 3, dev, what)
-    T, H, d = t.shape
-    row, head, col = st
-    if col != 1 or (head != d and H > 1):
-        raise ValueError(f"{what}: heads and columns must be contiguous")
+    T, H, d = shape
+    if t.is_contiguous():
+        return H * d
+    row, head, col = t.stride()
+    if col != 1 or (head != d and H > 1) or (T > 1 and row < H * d):
+        raise ValueError(f"{what}: heads and columns must be contiguous, and rows must not overlap")
     return row if T > 1 else H * d
 
 
 def _table_stride(t, what):
-    row, col = t.stride()
-    if col != 1 and t.shape[1] > 1:
-        raise ValueError(f"{what}: entries of a row must be contiguous")
-    return row if t.shape[0] > 1 else t.shape[1]
+    (rows, width), (row, col) = t.shape, t.stride()
+    if (col != 1 and width > 1) or (row < width and rows > 1):
+        raise ValueError(f"{what}: entries of a row must be contiguous, and rows must not overlap")
+    return row if rows > 1 else width
 
 
 def _paged(k_pages, v_pages, page_table, seq_lens, dev):
+    """The spts_paged_cache, as bytes, and (Hkv, d, B, page size, pages of a table row)."""
     index = -1 if dev.index is None else dev.index
-    shape, table = k_pages.shape, page_table.shape
+    shape, table, lens = k_pages.shape, page_table.shape, seq_lens.shape
     if not (k_pages.dtype is _BF and v_pages.dtype is _BF and page_table.dtype is _I32 and seq_lens.dtype is _I32 and
-            len(shape) == 4 and len(table) == 2 and seq_lens.dim() == 1 and k_pages.get_device() == index and
+            len(shape) == 4 and len(table) == 2 and len(lens) == 1 and k_pages.get_device() == index and
             v_pages.get_device() == index and page_table.get_device() == index and seq_lens.get_device() == index):
         _want(k_pages, _BF, 4, dev, "k_pages")
         _want(v_pages, _BF, 4, dev, "v_pages")
         _want(page_table, _I32, 2, dev, "page_table")
         _want(seq_lens, _I32, 1, dev, "seq_lens")
     n, page, Hkv, d = shape
-    st = k_pages.stride()
-    if v_pages.shape != shape or v_pages.stride() != st or \
-            (st[1:] != (Hkv * d, d, 1) and any(k > 1 and x != y for k, x, y in zip(shape[1:], st[1:], (Hkv * d, d, 1)))):
-        raise ValueError("k_pages and v_pages must be alike, and contiguous inside a page")
+    page_stride = 0
+    if v_pages.shape != shape or not (k_pages.is_contiguous() and v_pages.is_contiguous()):
+        st = k_pages.stride()
+        if v_pages.shape != shape or v_pages.stride() != st or \
+                any(k > 1 and x != y for k, x, y in zip(shape[1:], st[1:], (Hkv * d, d, 1))):
+            raise ValueError("k_pages and v_pages must be alike, and contiguous inside a page")
+        if n > 1:
+            page_stride = st[0]
+            if page_stride < page * Hkv * d:
+                raise ValueError("k_pages and v_pages: pages must not overlap")
     rows, width = table
-    row, col = page_table.stride()
-    B = seq_lens.shape[0]
-    if rows != B or (B > 1 and seq_lens.stride(0) != 1) or (col != 1 and width > 1):
+    B = lens[0]
+    row = width
+    alike = rows == B and seq_lens.is_contiguous()
+    if alike and not page_table.is_contiguous():
+        row, col = page_table.stride()
+        if B == 1:
+            row = width
+        alike = (col == 1 or width == 1) and row >= width
+    if not alike:
         raise ValueError("page_table and seq_lens need one row and one contiguous entry per sequence")
-    c = PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), n, st[0] if n > 1 else 0, page, B, page_table.data_ptr(),
-                   width, row if B > 1 else width, seq_lens.data_ptr())
-    c.Hkv, c.d = Hkv, d
-    return c
+    return _pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), n, page_stride, page, B, page_table.data_ptr(), width,
+                       row, seq_lens.data_ptr()), Hkv, d, B, page, width
 
 
 def _vector(t, n, dev, what):
     """Address of n contiguous int32 entries."""
-    if t.dtype is not _I32 or t.shape != (n,) or t.get_device() != dev.index or (n > 1 and t.stride(0) != 1):
+    if t.dtype is not _I32 or t.shape != (n,) or t.get_device() != dev.index or not t.is_contiguous():
         _want(t, _I32, 1, dev, what)
         raise ValueError(f"{what}: need {n} contiguous entries, got {tuple(t.shape)} with strides {t.stride()}")
     return t.data_ptr()
 
 
-def _scores(weights, c, Hkv, dev, what):
+def _scores(weights, cache, dev, what):
     """(Hs, stride between rows [b, hs], slots) of a weights tensor."""
     if weights.dtype is not _F32 or weights.dim() != 3 or weights.get_device() != dev.index:
         _want(weights, _F32, 3, dev, what)
+    Hkv, rows = cache[1], cache[3]
     B, Hs, n = weights.shape
     sb, sh, sn = weights.stride()
     row = sh if Hs > 1 else sb if B > 1 else n
-    if B != c.B or Hs not in (1, Hkv):
+    if B != rows or Hs not in (1, Hkv):
         raise ValueError(f"{what}: need [B, 1 or Hkv, slots], got {tuple(weights.shape)}")
     if (n > 1 and sn != 1) or (B > 1 and sb != Hs * row):
         raise ValueError(f"{what}: need evenly spaced rows of contiguous entries")
@@ -473,7 +493,7 @@ def _own_ws(ws, nbytes, dev):
     the cached one's address after a larger call has replaced it."""
     if ws is not None:
         return _want(ws, torch.uint8, 1, dev, "ws")
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing():
         raise ValueError("pass a workspace of your own (ws) while a graph is captured")
     t = _ws_cache.get(dev)
     return t if t is not None and t.numel() >= nbytes else workspace(nbytes, dev)
@@ -484,7 +504,7 @@ def _elsewhere(dev, who):
     launches, stream and workspace are those of its tensors' device."""
     if dev.type != "cuda":
         raise ValueError(f"{who}: tensors must be on a CUDA device, got {dev}")
-    return dev.index != torch.cuda.current_device()
+    return dev.index != _current_device()
 
 
 @functools.lru_cache(maxsize=256)
@@ -507,12 +527,12 @@ def spts_cache_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, cu_n
             return spts_cache_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, cu_new, pos, theta, ws)
     k_stride, v_stride = _packed(k_new, dev, "k_new"), _packed(v_new, dev, "v_new")
     T, Hkv, d = shape = k_new.shape
-    c = _paged(k_pages, v_pages, page_table, seq_lens, dev)
-    if v_new.shape != shape or Hkv != c.Hkv or d != c.d:
+    cache, heads, dim, B, _, _ = _paged(k_pages, v_pages, page_table, seq_lens, dev)
+    if v_new.shape != shape or Hkv != heads or d != dim:
         raise ValueError("k_new, v_new and the pages must agree in tokens, heads and head dim")
-    cu, at = _vector(cu_new, c.B + 1, dev, "cu_new"), None if pos is None else _vector(pos, T, dev, "pos")
+    cu, at = _vector(cu_new, B + 1, dev, "cu_new"), None if pos is None else _vector(pos, T, dev, "pos")
     ws = _own_ws(ws, 256, dev)
-    check(lib.spts_cache_append(C.byref(_bf16_desc(Hkv, Hkv, d)), C.byref(c), k_new.data_ptr(), k_stride,
+    check(lib.spts_cache_append(C.byref(_bf16_desc(Hkv, Hkv, d)), cache, k_new.data_ptr(), k_stride,
                                 v_new.data_ptr(), v_stride, cu, T, at, theta, ws.data_ptr(), _raw_stream(dev.index)))
 
 
@@ -533,12 +553,12 @@ def spts_paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_q, scale=
             return spts_paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_q, scale, out, lse, weights, ws)
     q_stride = _packed(q, dev, "q")
     T, Hq, d = shape = q.shape
-    c = _paged(k_pages, v_pages, page_table, seq_lens, dev)
-    Hkv = c.Hkv
-    if d != c.d:
+    cache = _paged(k_pages, v_pages, page_table, seq_lens, dev)
+    view, Hkv, dim, B, page, max_pages = cache
+    if d != dim:
         raise ValueError("q and the pages must agree in head dim")
     if out is None:
-        o, o_stride = q.new_empty(shape), 0
+        o, o_stride = torch.empty_like(q), 0
     else:
         o, o_stride = out, _packed(out, dev, "out")
         if o.shape != shape:
@@ -546,13 +566,13 @@ def spts_paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_q, scale=
     e = q.new_empty((T, Hq), dtype=_F32) if lse else None
     Hs = stride = 0
     if weights is not None:
-        Hs, stride, n = _scores(weights, c, Hkv, dev, "weights")
-        if n < c.max_pages * c.page_size:
+        Hs, stride, n = _scores(weights, cache, dev, "weights")
+        if n < max_pages * page:
             raise ValueError("weights: need a slot for every slot of a page table row")
-    ws = _own_ws(ws, _attention_ws_bytes(Hq, Hkv, d, c.B, c.page_size, c.max_pages, T, 0 if weights is None else 1), dev)
+    ws = _own_ws(ws, _attention_ws_bytes(Hq, Hkv, d, B, page, max_pages, T, 0 if weights is None else 1), dev)
     a = _bf16_desc(Hq, Hkv, d, 0.0 if scale is None else float(scale))
-    check(lib.spts_paged_attention(C.byref(a), C.byref(c), q.data_ptr(), q_stride, _vector(cu_q, c.B + 1, dev, "cu_q"),
-                                   T, o.data_ptr(), o_stride, None if e is None else e.data_ptr(),
+    check(lib.spts_paged_attention(C.byref(a), view, q.data_ptr(), q_stride, _vector(cu_q, B + 1, dev, "cu_q"), T,
+                                   o.data_ptr(), o_stride, None if e is None else e.data_ptr(),
                                    None if weights is None else weights.data_ptr(), Hs, stride, ws.data_ptr(),
                                    ws.numel(), _raw_stream(dev.index)))
     return (o, e) if lse else o
@@ -574,26 +594,26 @@ def spts_cache_evict(k_pages, v_pages, page_table, seq_lens, weights, keep, sink
         with torch.cuda.device(dev):
             return spts_cache_evict(k_pages, v_pages, page_table, seq_lens, weights, keep, sink, recent, dst_table,
                                     weights_out, new_lens, kept, ws)
-    c = _paged(k_pages, v_pages, page_table, seq_lens, dev)
-    Hkv, d = c.Hkv, c.d
-    Hs, stride, n = _scores(weights, c, Hkv, dev, "weights")
-    if n < c.max_pages * c.page_size:
+    cache = _paged(k_pages, v_pages, page_table, seq_lens, dev)
+    view, Hkv, d, B, page, max_pages = cache
+    Hs, stride, n = _scores(weights, cache, dev, "weights")
+    if n < max_pages * page:
         raise ValueError("weights: need a slot for every slot of a page table row")
     dst = page_table if dst_table is None else _want(dst_table, _I32, 2, dev, "dst_table")
-    if dst.shape[0] != c.B:
+    if dst.shape[0] != B:
         raise ValueError("dst_table: need one row per sequence")
     if weights_out is None:
-        weights_out = weights if dst_table is None else weights.new_empty((c.B, Hs, dst.shape[1] * c.page_size))
-    Ho, out_stride, m = _scores(weights_out, c, Hkv, dev, "weights_out")
+        weights_out = weights if dst_table is None else weights.new_empty((B, Hs, dst.shape[1] * page))
+    Ho, out_stride, m = _scores(weights_out, cache, dev, "weights_out")
     if Ho != Hs or m != out_stride:
         raise ValueError("weights_out: need contiguous rows, as many as weights has")
     if new_lens is None:
-        new_lens = seq_lens.new_empty(c.B)
-    idx = seq_lens.new_empty((c.B, Hs, keep)) if kept else None
-    ws = _own_ws(ws, lib.spts_cache_evict_workspace(C.byref(c), Hs, keep), dev)
-    check(lib.spts_cache_evict(C.byref(_bf16_desc(Hkv, Hkv, d)), C.byref(c), weights.data_ptr(), Hs, stride, keep, sink,
+        new_lens = seq_lens.new_empty(B)
+    idx = seq_lens.new_empty((B, Hs, keep)) if kept else None
+    ws = _own_ws(ws, lib.spts_cache_evict_workspace(view, Hs, keep), dev)
+    check(lib.spts_cache_evict(C.byref(_bf16_desc(Hkv, Hkv, d)), view, weights.data_ptr(), Hs, stride, keep, sink,
                                recent, dst.data_ptr(), dst.shape[1], _table_stride(dst, "dst_table"),
-                               weights_out.data_ptr(), out_stride, _vector(new_lens, c.B, dev, "new_lens"),
+                               weights_out.data_ptr(), out_stride, _vector(new_lens, B, dev, "new_lens"),
                                None if idx is None else idx.data_ptr(), ws.data_ptr(), ws.numel(),
                                _raw_stream(dev.index)))
     return (new_lens, weights_out, idx) if kept else (new_lens, weights_out)
