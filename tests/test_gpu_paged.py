@@ -489,6 +489,31 @@ def test_weights_over_all_heads_with_a_wide_table(new):
     check_attention(c, new, 16, 8, 64, seed=47, each=False)
 
 
+@pytest.mark.parametrize("each", [True, False])
+@pytest.mark.parametrize("B,Hq,Hkv,d", [(7, 64, 1, 128), (40, 128, 2, 64), (110, 128, 2, 64), (3, 1, 1, 128)])
+def test_weights_of_few_and_many_key_tiles(B, Hq, Hkv, d, each):
+    # up to four K tiles per SM are dealt out one by one, more by equal cost; one to four warpgroups to a tile
+    lens = [1 + (37 * i * i + 131 * i) % 900 for i in range(B)]
+    new = [min(1 + i % 9 if Hq > 1 else 300 * (i + 1), n) for i, n in enumerate(lens)]
+    c = Cache(lens, 32, Hkv, d, seed=61)
+    check_attention(c, new, Hq, Hkv, d, seed=62, each=each)
+
+
+def test_weights_twice_give_the_same_bits():
+    lens = [1 + (53 * i * i + 17 * i) % 700 for i in range(60)]
+    new = [min(1 + 7 * (i % 30), n) for i, n in enumerate(lens)]
+    c = Cache(lens, 64, 4, 128, seed=63)
+    cu, q = packed(new, 16, 128, 64)
+    runs = []
+    for _ in range(4):
+        w = torch.zeros(60, 1, c.table.shape[1] * 64, device="cuda")
+        S.spts_paged_attention(q, *c.args(), i32(cu), weights=w)
+        runs.append(w)
+    assert all(torch.equal(w, runs[0]) for w in runs)
+    # a row's weights add up to 1: each is off by 2 (d + 4) 2^-23 of the scores' absolute products (about 14), and 2^-19
+    assert abs(float(runs[0].double().sum()) - 16 * sum(new)) < 1e-3 * 16 * sum(new)
+
+
 # ------------------------------------------------------------------ streams, graphs, a run of all
 def test_two_streams_with_workspaces_of_their_own():
     cs = [Cache([700 + 50 * i, 90], 16, 2, 128, seed=31 + i) for i in range(2)]

@@ -49,6 +49,9 @@ extern "C" int first_cut(const PlanCut *cut, int r) { return plan_first_cut(*cut
 extern "C" void piece_of(const PlanCut *cut, int r, int i, int *out) {
   plan_piece_of(*cut, r, i, out[0], out[1], out[2], out[3]);
 }
+extern "C" int64_t keys_cost(int n, int L, int tq, int64_t j) { return plan_keys_cost(PlanSeq{n, L}, tq, j); }
+extern "C" int keys_at(int n, int L, int tq, int tiles, int64_t x) { return plan_keys_at(PlanSeq{n, L}, tq, tiles, x); }
+extern "C" int sharers(int tiles, int q_tiles) { return plan_sharers(tiles, q_tiles); }
 extern "C" void tiles_of(int off, int end, int c, int tiles, int *out) { plan_tiles(off, end, c, tiles, out[0], out[1]); }
 """
 
@@ -165,3 +168,32 @@ def test_positions_past_32_bits(plan):
     last = rows[-1]
     assert (last[1], last[2], last[3]) == (7, 0, 7) and last[5] == last[6] == (1 << 30) // 128
     assert int((rows[:, 5] - rows[:, 4]).astype(np.int64).sum()) == 64 * ((1 << 30) // 128)
+
+
+def test_cost_of_the_key_tiles_of_a_second_pass(plan):
+    plan.keys_cost.restype = C.c_int64
+    plan.keys_cost.argtypes = [C.c_int, C.c_int, C.c_int, C.c_int64]
+    plan.keys_at.argtypes = [C.c_int] * 4 + [C.c_int64]
+    rng = np.random.default_rng(6)
+    for _ in range(300):
+        tq = 128 // int(rng.choice([1, 2, 3, 5, 7, 8, 64, 128]))
+        n = int(rng.integers(1, rng.choice([2, 40, 900])))
+        L = max(1, n + int(rng.integers(-5, rng.choice([1, 200, 4000]))))
+        tiles = -(-L // 128)
+        cost = [(-(-n // tq) + 2) * tq - max(128 * j - (L - n), 0) for j in range(tiles)]
+        assert min(cost) > 0
+        ends = np.concatenate([[0], np.cumsum(cost)])
+        assert [plan.keys_cost(n, L, tq, j) for j in range(tiles + 1)] == ends.tolist()
+        for x in rng.integers(0, int(ends[-1]) + 2, 20).tolist() + ends.tolist():
+            assert plan.keys_at(n, L, tq, tiles, x) == min(int(np.searchsorted(ends, x)), tiles)
+    # past 32 bits
+    n = L = 1 << 24
+    tiles = n // 128
+    assert plan.keys_cost(n, L, 32, tiles) == tiles * (n + 64) - 64 * tiles * (tiles - 1)
+
+
+def test_warpgroups_that_share_a_key_tile(plan):
+    for tiles in (1, 2, 3, 4):
+        for q in range(1, 9):
+            s = plan.sharers(tiles, q)
+            assert 1 <= s <= q and s * tiles <= 4 and (s == q or (s + 1) * tiles > 4)

@@ -1115,12 +1115,16 @@ spts_status launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   note_launch();
   SPTS_CUDA_TRY(cudaGetLastError());
   if (ctas > 1 && !p.whole) {
-    // CTAs per unit: one turn of its warps for the largest window
-    constexpr int ROWS = MODE == FULL ? 4 : 1, DEEP = MODE == FULL ? 2 : 8;
-    const int most = (p.T < p.w ? p.T : p.w) * p.G, turn = JOIN_WARPS * ROWS;
+    // Few units are cut into many pieces each: a row to a warp and eight pieces
+    // on their way, as for steps (28 rows of 2 heads over 4574 slots, 74
+    // pieces per unit: 26 us, and 47 with four rows to a warp and two pieces);
+    // CTAs per unit: one turn of its warps for the largest window.
+    const int64_t units = (static_cast<int64_t>(p.T) / p.w + p.c.B) * p.c.Hkv;
+    const bool deep = MODE != FULL || units * 8 <= ctas;
+    const int most = (p.T < p.w ? p.T : p.w) * p.G, turn = JOIN_WARPS * (deep ? 1 : 4);
     const int split = MODE == FULL ? (most + turn - 1) / turn : 1;
-    SPTS_TRY(launch_behind(paged_combine_kernel<D, ROWS, DEEP>, dim3(ctas - 1, p.max_groups, split), 32 * JOIN_WARPS, s,
-                           0, p, ctas));
+    SPTS_TRY(launch_behind(deep ? paged_combine_kernel<D, 1, 8> : paged_combine_kernel<D, 4, 2>,
+                           dim3(ctas - 1, p.max_groups, split), 32 * JOIN_WARPS, s, 0, p, ctas));
   }
   return SPTS_OK;
 }

@@ -223,4 +223,31 @@ SPTS_HD void plan_piece_of(const PlanCut &cut, int r, int i, int &range, int &sl
   end = static_cast<int>(e < c ? e : c);
 }
 
+// The accumulated weights' pass: K tiles of a head, each with the Q tiles (of tq
+// tokens) that see any of its slots.  Cost of a head's first j tiles, in
+// tokens, with PLAN_KEYS Q tiles for what a K tile costs by itself; the tokens
+// in front of a tile's first slot do not see it.
+constexpr int PLAN_KEYS = 2;
+SPTS_HD int64_t plan_keys_cost(const PlanSeq &s, int tq, int64_t j) {
+  const int64_t base = s.L - s.n, first = base < 0 ? 0 : base / PLAN_TILE + 1;  // the first tile some tokens miss
+  int64_t cost = j * (static_cast<int64_t>(plan_windows(s.n, tq)) + PLAN_KEYS) * tq;
+  if (j > first) cost -= (PLAN_TILE / 2) * (first + j - 1) * (j - first) - base * (j - first);
+  return cost;
+}
+
+// The first of a head's `tiles` tiles that begins at cost x or later (`tiles`: none).
+SPTS_HD int plan_keys_at(const PlanSeq &s, int tq, int tiles, int64_t x) {
+  int lo = 0, hi = tiles;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (plan_keys_cost(s, tq, mid) >= x) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Units whose K tiles leave warpgroups over (of four) share out their Q tiles:
+// warpgroup x takes K tile x % tiles and every plan_sharers-th Q tile.
+SPTS_HD int plan_sharers(int tiles, int q_tiles) { return plan_min(tiles > 2 ? 1 : 4 / tiles, q_tiles); }
+
 }  // namespace spts

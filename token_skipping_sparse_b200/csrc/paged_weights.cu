@@ -9,14 +9,19 @@
 // of four warpgroups; they stay in shared memory while the Q tiles of the
 // sequence (128 / G tokens x G heads each) stream past all four.  (With two K
 // tiles per Q tile the Q loads were what everything waited for: without any
-// exponential 250 rows over 32K slots still took 90 of 126 us.)  Bound by the
+// exponential 250 rows over 32K slots still took 90 of 126 us.)  With one or
+// two K tiles the warpgroups share out the Q tiles instead, and their sums are
+// added in order at the end: 7
+// sequences of 685 new tokens in 738, 2 heads of 8 (84 K tiles), 68 -> 46 us.
+// Bound by the
 // exponentials (16384 per K and Q tile: 1024 cycles of the MUFU pipe against
 // 512 of the MMA) when there are many rows, by reading K when there are few.
 // All exponentials are the MUFU pipe's: the output is fp32.
 //   warp 0  TMA, warp 1  MMA, warp 3  hands out the units, warps 4..19  four
 //   warpgroups, one per K tile
-// The K tiles of all sequences and heads, weighted with their Q tiles, are
-// shared out evenly; a CTA's share is cut into units at heads and fours.
+// The K tiles of all sequences and heads, weighted with the Q tiles that see
+// them, are shared out evenly; a CTA's share is cut into units at heads and
+// fours.
 // With one weight row for all heads (Hs = 1) the units of a slot's KV heads
 // leave partial sums that a last kernel adds in order, as long as their scratch
 // stays below SPLIT_BYTES; beyond, a unit walks all its heads itself.
@@ -30,7 +35,9 @@ namespace {
 
 constexpr int THREADS = 640;
 constexpr int REG_LOW = 56, REG_HIGH = 104;  // 56 + 4 x 104 <= 5 x 96, the launch allocation
-constexpr int WG = 4;  // warpgroups, and K tiles of a unit
+constexpr int WG = 4;  // warpgroups, and K tiles of a unit at most
+constexpr int ROUNDS = 4;    // K tiles of a CTA, at most, that are dealt out one by one
+constexpr int LISTED = 640;  // and in all
 constexpr int BKV = PLAN_TILE;
 constexpr int CHUNK = 128 * 64 * 2;
 constexpr int MAX_SEQ = 1024;
@@ -47,19 +54,24 @@ struct Unit {
   int first;         // packed row of its first new token
   int g0, slot0;     // first KV head, first slot
   int tiles;         // K tiles
+  int share;         // warpgroups that share a K tile's Q tiles
   int q0, q1;        // Q tiles that see any of its slots
 };
 
 struct Tail {
-  int64_t before[MAX_SEQ + 1];  // cost of the sequences before: K tiles x heads x Q tiles
+  int64_t before[MAX_SEQ + 1];  // cost of the sequences before, all heads (few K tiles: how many)
   PlanSeq seq[MAX_SEQ];
   int first[MAX_SEQ];
   alignas(16) float lse[WG][2][128];  // per warpgroup, by turns: -lse (log2) of the Q tile's rows
   uint64_t q_full[2], q_empty[2], k_full[WG], k_empty[WG];
-  uint64_t s_full[WG], s_free[WG], lse_full[2 * WG], drain;
+  float join[WG][128];  // the sums of a warpgroup that shares the K tile of another one
+  uint64_t s_full[WG], s_free[WG], lse_full[2 * WG], join_full[WG], join_free[WG], drain;
   uint64_t item_full[ITEMS], item_empty[ITEMS];
   Unit item[ITEMS];
   uint32_t tmem;
+  int listed;        // all K tiles, where they are dealt out one by one; otherwise 0
+  int mine[ROUNDS];  // then: this CTA's, or -1
+  alignas(16) int cost[LISTED];
   int abort_flag;
 };
 
@@ -85,7 +97,52 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 __device__ __forceinline__ int k_tiles(int L) { return (L + BKV - 1) / BKV; }
-__device__ __forceinline__ int q_tiles(int n, int tq) { return (n + tq - 1) / tq; }
+
+// K tile i of a call with few of them.
+struct KeyTile {
+  int b, g, j;
+};
+__device__ __forceinline__ KeyTile key_tile(const Tail &t, const Params &p, int i) {
+  int lo = 0, hi = p.c.B;
+  while (lo < hi) {  // the first sequence that ends behind it
+    const int mid = (lo + hi) >> 1;
+    if (t.before[mid + 1] <= i) lo = mid + 1;
+    else hi = mid;
+  }
+  const int in = i - static_cast<int>(t.before[lo]), tiles = k_tiles(t.seq[lo].L);
+  return KeyTile{lo, in / tiles, in % tiles};
+}
+
+// Few K tiles, whose costs differ: an equal share of the cost would end in the
+// middle of most of them (148 alike, a few cheaper, on 148 CTAs: 332 us, and 210
+// one by one).  In the order of falling cost they go round the CTAs, to and fro.
+// All threads.
+__device__ __forceinline__ void deal_out(Tail &t, const Params &p) {
+  const int total = t.listed, ctas = gridDim.x, x = blockIdx.x;
+  for (int i = threadIdx.x; i < LISTED; i += THREADS) {
+    int cost = 0;
+    if (i < total) {
+      const KeyTile k = key_tile(t, p, i);
+      cost = static_cast<int>(plan_keys_cost(t.seq[k.b], p.tq, k.j + 1) - plan_keys_cost(t.seq[k.b], p.tq, k.j));
+    }
+    t.cost[i] = cost;
+  }
+  if (threadIdx.x < ROUNDS) t.mine[threadIdx.x] = -1;
+  __syncthreads();
+  const int i = threadIdx.x;
+  if (i < total) {
+    const int4 *cost = reinterpret_cast<const int4 *>(t.cost);
+    const int own = t.cost[i];
+    int rank = 0;  // tiles in front of this one
+    for (int k = 0; k < total; k += 4) {
+      const int4 c = cost[k >> 2];
+      rank += (c.x + (k < i) > own) + (c.y + (k + 1 < i) > own) + (c.z + (k + 2 < i) > own) + (c.w + (k + 3 < i) > own);
+    }
+    const int round = rank / ctas, at = rank - round * ctas;
+    if (x == (round & 1 ? ctas - 1 - at : at)) t.mine[round] = i;
+  }
+  __syncthreads();
+}
 
 // Warp 3, one lane: this CTA's units, handed to the other warps through a
 // ring.  K tiles are ordered by (sequence, head, slot); a tile belongs to the
@@ -102,33 +159,55 @@ __device__ __forceinline__ void walk(Tail &t, const Params &p) {
         mbar_wait_long(&t.item_empty[i], ((count / ITEMS) & 1) ^ 1, abort_flag, p.status, p.wait_ns, 0x60u);
     return ok ? &t.item[i] : nullptr;
   };
-  for (int b = 0; b < p.c.B && t.before[b] < hi; ++b) {
-    if (t.before[b + 1] <= lo) continue;
+  // `take` K tiles of a head from tile j on; false: the kernel is on its way out
+  auto hand_out = [&](int b, int g, int j, int take) -> bool {
+    Unit *r = place();
+    if (r == nullptr) return false;
     const PlanSeq s = t.seq[b];
-    const int tiles = k_tiles(s.L), cost = q_tiles(s.n, p.tq);
-    if (tiles == 0 || cost == 0) continue;
+    r->more = 1;
+    r->b = b;
+    r->n = s.n;
+    r->L = s.L;
+    r->first = t.first[b];
+    r->g0 = g * p.unit_heads;
+    r->slot0 = j * BKV;
+    r->tiles = take;
+    r->q0 = max(j * BKV - (s.L - s.n), 0) / p.tq;  // the first token that sees the first slot
+    r->q1 = plan_windows(s.n, p.tq);               // > q0: the last token sees every slot below L
+    r->share = plan_sharers(take, r->q1 - r->q0);
+    mbar_arrive(&t.item_full[count % ITEMS]);
+    ++count;
+    return true;
+  };
+  if (t.listed) {
+    for (int i = 0; i < ROUNDS && t.mine[i] >= 0; ++i) {
+      const KeyTile k = key_tile(t, p, t.mine[i]);
+      if (!hand_out(k.b, k.g, k.j, 1)) return;
+    }
+  }
+  int b0 = t.listed ? p.c.B : 0;
+  for (int end = p.c.B; b0 < end;) {  // the first sequence that ends behind lo
+    const int mid = (b0 + end) >> 1;
+    if (t.before[mid + 1] <= lo) b0 = mid + 1;
+    else end = mid;
+  }
+  for (int b = b0; b < p.c.B && t.before[b] < hi; ++b) {
+    const PlanSeq s = t.seq[b];
+    const int tiles = k_tiles(s.L);
+    if (tiles == 0 || s.n == 0) continue;
     // tiles [from, to) of the sequence's tiles of all heads begin in this share
-    const int64_t all = static_cast<int64_t>(tiles) * heads;
-    const int64_t x = lo - t.before[b], y = hi - t.before[b];
-    const int64_t from = x <= 0 ? 0 : (x + cost - 1) / cost, to = y >= all * cost ? all : (y + cost - 1) / cost;
+    const int64_t head = plan_keys_cost(s, p.tq, tiles);
+    auto index_at = [&](int64_t x) -> int64_t {
+      if (x <= 0) return 0;
+      const int64_t g = plan_div(x, head);
+      return g >= heads ? static_cast<int64_t>(heads) * tiles : g * tiles + plan_keys_at(s, p.tq, tiles, x - g * head);
+    };
+    const int64_t from = index_at(lo - t.before[b]), to = index_at(hi - t.before[b]);
     int g = static_cast<int>(from / tiles), j = static_cast<int>(from - static_cast<int64_t>(g) * tiles);
     for (int64_t k = from; k < to;) {
       const int64_t left = to - k;
-      const int take = min(min(WG, tiles - j), left < WG ? static_cast<int>(left) : WG);
-      Unit *r = place();
-      if (r == nullptr) return;
-      r->more = 1;
-      r->b = b;
-      r->n = s.n;
-      r->L = s.L;
-      r->first = t.first[b];
-      r->g0 = g * p.unit_heads;
-      r->slot0 = j * BKV;
-      r->tiles = take;
-      r->q0 = max(j * BKV - (s.L - s.n), 0) / p.tq;  // the first token that sees the first slot
-      r->q1 = cost;                                  // > q0: the last token sees every slot below L
-      mbar_arrive(&t.item_full[count % ITEMS]);
-      ++count;
+      const int take = min(tiles - j, left < WG ? static_cast<int>(left) : WG);
+      if (!hand_out(b, g, j, take)) return;
       k += take;
       j += take;
       if (j == tiles) {
@@ -149,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                          const __grid_constant__ Params p) {
   constexpr int CH = D / 64, TILE = CH * CHUNK;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t *sQ = smem, *sK = smem + 2 * TILE;  // a ring of 2 Q tiles; the unit's K tiles
+  uint8_t *sQ = smem, *sK = smem + 2 * TILE;  // a ring of 2 Q tiles; one of K tiles
   Tail &t = *reinterpret_cast<Tail *>(smem + 6 * TILE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int *abort_flag = &t.abort_flag;
@@ -171,6 +250,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&t.s_free[i], 4);  // here and below: one arrival per warp
       mbar_init(&t.lse_full[2 * i], 4);
       mbar_init(&t.lse_full[2 * i + 1], 4);
+      mbar_init(&t.join_full[i], 4);
+      mbar_init(&t.join_free[i], 4);
     }
     for (int i = 0; i < ITEMS; ++i) {
       mbar_init(&t.item_full[i], 1);
@@ -192,12 +273,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   __syncthreads();
   if (warp == 0) {
-    int64_t run = 0;
+    const int heads = p.c.Hkv / p.unit_heads;
+    int64_t run = 0, k_total = 0;
+    for (int b = lane; b < p.c.B; b += 32)
+      if (t.seq[b].n > 0) k_total += static_cast<int64_t>(k_tiles(t.seq[b].L)) * heads;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) k_total += __shfl_xor_sync(0xffffffffu, k_total, o);
+    const bool few = k_total <= ROUNDS * static_cast<int64_t>(gridDim.x) && k_total <= LISTED;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
       const int b = b0 + lane;
       int64_t x = 0;
-      if (b < p.c.B)
-        x = static_cast<int64_t>(k_tiles(t.seq[b].L)) * (p.c.Hkv / p.unit_heads) * q_tiles(t.seq[b].n, p.tq);
+      if (b < p.c.B && t.seq[b].n > 0) {
+        const int tiles = k_tiles(t.seq[b].L);
+        x = (few ? tiles : plan_keys_cost(t.seq[b], p.tq, tiles)) * heads;
+      }
       int64_t incl = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -207,11 +296,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (b < p.c.B) t.before[b] = run + incl - x;
       run += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) t.before[p.c.B] = run;
+    if (lane == 0) {
+      t.before[p.c.B] = run;
+      t.listed = few ? static_cast<int>(k_total) : 0;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (t.listed) deal_out(t, p);
   const uint32_t tmem = uniform(t.tmem);
   // launched while the attention still runs: nothing that it writes (lse, the
   // scratch) is touched before this
@@ -231,8 +324,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int page = 1 << p.c.page_shift, rows = min(page, BKV), boxes = BKV / rows;
     const bool mine = lane < boxes * CH;
     const int box = lane / CH, ch = lane % CH;
-    int qc = 0;
-    uint32_t q_issued = 0, q_par = 0, k_issued = 0, k_par = 0;  // k_par: the parity of each K tile's next phase
+    int qs = 0, k0 = 0;  // where the next Q and K tiles go
+    uint32_t qph = 0;
+    uint32_t q_issued = 0, q_par = 0, k_issued = 0, k_par = 0;  // k_par: the parity of each K place's next phase
     bool ok = true;
     auto wait_all = [&](uint64_t *bar, uint32_t parity, uint32_t where) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns, where));
@@ -258,19 +352,19 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int w = 0; w < WG; ++w) {
           if (w >= tiles || !ok) break;
-          ok = wait_all(&t.k_empty[w], ((k_par >> w) & 1u) ^ 1u, 0x61u);
+          const int x = (k0 + w) & (WG - 1);
+          ok = wait_all(&t.k_empty[x], ((k_par >> x) & 1u) ^ 1u, 0x61u);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&t.k_full[w], TILE);
+          if (lane == 0) mbar_arrive_expect_tx(&t.k_full[x], TILE);
           __syncwarp();
           if (mine)
-            tma_load_4d(sK + w * TILE + ch * CHUNK + box * rows * 128, &tmK, &t.k_full[w], ch * 64, g,
+            tma_load_4d(sK + x * TILE + ch * CHUNK + box * rows * 128, &tmK, &t.k_full[x], ch * 64, g,
                         (slot0 + w * BKV) & (page - 1), at[w]);
-          k_issued |= 1u << w;
-          k_par ^= 1u << w;
+          k_issued |= 1u << x;
+          k_par ^= 1u << x;
         }
-        for (int q = q0; ok && q < q1; ++q, ++qc) {
-          const int qs = qc & 1;
-          const uint32_t qph = (qc >> 1) & 1;
+        k0 = (k0 + tiles) & (WG - 1);
+        for (int q = q0; ok && q < q1; ++q) {
           ok = wait_all(&t.q_empty[qs], qph ^ 1u, 0x62u);
           if (!ok) break;
           if (lane == 0) {
@@ -280,6 +374,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           q_issued |= 1u << qs;
           q_par = (q_par & ~(1u << qs)) | (qph << qs);
+          qs ^= 1;
+          qph ^= qs ^ 1;
         }
       }
     }
@@ -293,8 +389,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == 1) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_LOW));
     constexpr uint32_t idesc = idesc_bf16_f32(BKV, 128, 0, 0);
-    int qc = 0;
-    uint32_t k_par = 0, s_par = 0;  // per K tile: parity of its next load, of its next S
+    int qs = 0, k0 = 0;
+    uint32_t qph = 0, k_par = 0, s_par = 0;  // parity of the next load of each K place, of the next S of each warpgroup
     bool ok = true;
     auto wait_all = [&](uint64_t *bar, uint32_t parity, uint32_t where) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.wait_ns, where));
@@ -302,32 +398,37 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; ok; ++i) {
       const Unit *un = take(i);
       if (!un) break;
-      const int n = uniform(un->q1 - un->q0), tiles = uniform(un->tiles);
+      const int n = uniform(un->q1 - un->q0), tiles = uniform(un->tiles), share = uniform(un->share);
       give_back(i);
       for (int h = 0; ok && h < p.unit_heads; ++h) {
-        for (int q = 0; ok && q < n; ++q, ++qc) {
-          const int qs = qc & 1;
-          ok = wait_all(&t.q_full[qs], (qc >> 1) & 1, 0x64u);
+        int x = 0;  // first warpgroup of this Q tile
+        for (int q = 0; ok && q < n; ++q) {
+          ok = wait_all(&t.q_full[qs], qph, 0x64u);
           const uint32_t q_addr = smem_u32(sQ + qs * TILE);
           for (int w = 0; ok && w < tiles; ++w) {
-            if (q == 0) ok = wait_all(&t.k_full[w], (k_par >> w) & 1u, 0x63u);
-            ok = ok && wait_all(&t.s_free[w], ((s_par >> w) & 1u) ^ 1u, 0x65u);
+            const int kw = (k0 + w) & (WG - 1), wg = x + w;
+            if (q == 0) ok = wait_all(&t.k_full[kw], (k_par >> kw) & 1u, 0x63u);
+            ok = ok && wait_all(&t.s_free[wg], ((s_par >> wg) & 1u) ^ 1u, 0x65u);
             if (!ok) break;
-            s_par ^= 1u << w;
+            s_par ^= 1u << wg;
             tc_fence_after();
-            const uint32_t k_addr = smem_u32(sK + w * TILE);
+            const uint32_t k_addr = smem_u32(sK + kw * TILE);
 #pragma unroll
             for (int kk = 0; kk < 4 * CH; ++kk) {
               const uint64_t a = sdesc_k_sw128(k_addr + (kk >> 2) * CHUNK) + 2 * (kk & 3);
               const uint64_t b = sdesc_k_sw128(q_addr + (kk >> 2) * CHUNK) + 2 * (kk & 3);
-              mma_bf16_ss_w(tmem + w * 128, a, b, idesc, kk > 0);
+              mma_bf16_ss_w(tmem + wg * 128, a, b, idesc, kk > 0);
             }
-            tc_commit_w(&t.s_full[w]);
-            if (q + 1 == n) tc_commit_w(&t.k_empty[w]);
+            tc_commit_w(&t.s_full[wg]);
+            if (q + 1 == n) tc_commit_w(&t.k_empty[kw]);
           }
           if (ok) tc_commit_w(&t.q_empty[qs]);
+          x = x + tiles == share * tiles ? 0 : x + tiles;
+          qs ^= 1;
+          qph ^= qs ^ 1;
         }
-        k_par ^= (1u << tiles) - 1u;
+        for (int w = 0; w < tiles; ++w) k_par ^= 1u << ((k0 + w) & (WG - 1));
+        k0 = (k0 + tiles) & (WG - 1);
       }
     }
     tc_commit_w(&t.drain);
@@ -344,18 +445,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float c2 = p.scale_log2;
     const int rt = r / p.G, rh = r - rt * p.G;  // token and head of Q row r, whose lse this thread fetches
     uint32_t sc = 0;                            // S tiles of this warpgroup so far
+    uint32_t join_par = 0;                      // per warpgroup: parity of its next sums for another one
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const Unit *un = take(i);
       if (!un) break;
-      const bool on = wg < un->tiles;
-      const int n = un->n, L = un->L, q0 = un->q0, q1 = un->q1, g0 = un->g0, first = un->first;
-      const int slot = un->slot0 + wg * BKV + r, base = L - n;
+      const int tiles = uniform(un->tiles), share = uniform(un->share), part = wg / tiles;
+      const int n = un->n, L = un->L, q0 = un->q0 + part, q1 = un->q1, g0 = un->g0, first = un->first;
+      const int slot = un->slot0 + (wg - part * tiles) * BKV + r, base = L - n;
       const int64_t out_row = static_cast<int64_t>(un->b) * p.out_heads + (p.out_heads == 1 ? 0 : g0);
       float *w = p.out + out_row * p.out_stride + slot;
       give_back(i);
-      if (!on) continue;
-      const float old = p.add && slot < L ? *w : 0.f;
+      const uint32_t joined = join_par;
+      join_par ^= ((1u << (share * tiles)) - 1u) & ~((1u << tiles) - 1u);
+      if (part >= share) continue;
+      const float old = p.add && part == 0 && slot < L ? *w : 0.f;
       // lse of this thread's row of Q tile q, fetched a tile ahead
       auto lse_of = [&](int h, int q) -> float {
         const int tok = q * p.tq + rt;
@@ -365,11 +469,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
       float next = lse_of(0, q0), sum[4] = {0.f, 0.f, 0.f, 0.f};
       for (int h = 0; ok && h < p.unit_heads; ++h) {
-        for (int q = q0; q < q1; ++q, ++sc) {
+        for (int q = q0; q < q1; q += share, ++sc) {
           uint64_t *lse_full = &t.lse_full[2 * wg + (sc & 1)];
           t.lse[wg][sc & 1][r] = next;
           mbar_arrive_warp(lse_full);
-          next = q + 1 < q1 ? lse_of(h, q + 1) : h + 1 < p.unit_heads ? lse_of(h + 1, q0) : 0.f;
+          next = q + share < q1 ? lse_of(h, q + share) : h + 1 < p.unit_heads ? lse_of(h + 1, q0) : 0.f;
           ok = __all_sync(0xffffffffu, mbar_wait(lse_full, (sc >> 1) & 1, abort_flag, p.status, p.wait_ns, 0x66u));
           if (!ok) break;
           ok = __all_sync(0xffffffffu, mbar_wait(&t.s_full[wg], sc & 1, abort_flag, p.status, p.wait_ns, 0x67u));
@@ -377,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tc_fence_after();
           // rows of the tile that see the slot: tokens >= slot - base, up to the last one
           const int lo = (slot - base - q * p.tq) * p.G, hi = min(p.tq, n - q * p.tq) * p.G;
-          const bool masked = __any_sync(0xffffffffu, lo > 0) || hi < 128;
+          const bool early = __any_sync(0xffffffffu, lo > 0);  // some slot of this warp is behind some row
           const float4 *ls = reinterpret_cast<const float4 *>(t.lse[wg][sc & 1]);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
@@ -390,10 +494,16 @@ __global__ void __launch_bounds__(THREADS, 1)
               tc_fence_before();
               mbar_arrive_warp(&t.s_free[wg]);
             }
-            if (masked) {
+            if (early) {
+              if (__all_sync(0xffffffffu, lo >= half * 64 + 64)) continue;  // no slot of this warp is seen
 #pragma unroll
               for (int c = 0; c < 64; ++c)
-                if (half * 64 + c < lo || half * 64 + c >= hi) xr[c] = 0xff800000u;  // -inf
+                if (half * 64 + c < lo) xr[c] = 0xff800000u;  // -inf
+            }
+            if (hi < half * 64 + 64) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (half * 64 + c >= hi) xr[c] = 0xff800000u;
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -407,7 +517,24 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       if (!ok) break;
-      if (slot < L) *w = old + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (part > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&t.join_free[wg], ((joined >> wg) & 1u) ^ 1u, abort_flag, p.status,
+                                               p.wait_ns, 0x68u));
+        if (!ok) break;
+        t.join[wg][r] = total;
+        mbar_arrive_warp(&t.join_full[wg]);
+        continue;
+      }
+      for (int x = wg + tiles; ok && x < share * tiles; x += tiles) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&t.join_full[x], (joined >> x) & 1u, abort_flag, p.status, p.wait_ns,
+                                               0x69u));
+        if (!ok) break;
+        total += t.join[x][r];
+        mbar_arrive_warp(&t.join_free[x]);
+      }
+      if (!ok) break;
+      if (slot < L) *w = old + total;
     }
   }
   __syncthreads();
