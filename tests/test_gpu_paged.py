@@ -490,11 +490,12 @@ def test_weights_over_all_heads_with_a_wide_table(new):
 
 
 @pytest.mark.parametrize("each", [True, False])
-@pytest.mark.parametrize("B,Hq,Hkv,d", [(7, 64, 1, 128), (40, 128, 2, 64), (110, 128, 2, 64), (3, 1, 1, 128)])
+@pytest.mark.parametrize("B,Hq,Hkv,d", [(7, 64, 1, 128), (40, 128, 2, 64), (110, 128, 2, 64), (3, 1, 1, 128),
+                                        (5, 128, 1, 128)])
 def test_weights_of_few_and_many_key_tiles(B, Hq, Hkv, d, each):
-    # up to four K tiles per SM are dealt out one by one, more by equal cost; one to four warpgroups to a tile
+    # few K tiles with many Q tiles each go round one by one, others by equal cost; one to four warpgroups to a tile
     lens = [1 + (37 * i * i + 131 * i) % 900 for i in range(B)]
-    new = [min(1 + i % 9 if Hq > 1 else 300 * (i + 1), n) for i, n in enumerate(lens)]
+    new = [min(1 + i % 9 if Hkv > 1 else 30 * (i + 1) if Hq > 1 else 300 * (i + 1), n) for i, n in enumerate(lens)]
     c = Cache(lens, 32, Hkv, d, seed=61)
     check_attention(c, new, Hq, Hkv, d, seed=62, each=each)
 

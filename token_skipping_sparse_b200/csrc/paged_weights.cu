@@ -38,6 +38,7 @@ constexpr int REG_LOW = 56, REG_HIGH = 104;  // 56 + 4 x 104 <= 5 x 96, the laun
 constexpr int WG = 4;  // warpgroups, and K tiles of a unit at most
 constexpr int ROUNDS = 4;    // K tiles of a CTA, at most, that are dealt out one by one
 constexpr int LISTED = 640;  // and in all
+constexpr int LISTED_STEPS = 9;  // from so many Q tiles per K tile on
 constexpr int BKV = PLAN_TILE;
 constexpr int CHUNK = 128 * 64 * 2;
 constexpr int MAX_SEQ = 1024;
@@ -116,7 +117,9 @@ __device__ __forceinline__ KeyTile key_tile(const Tail &t, const Params &p, int 
 // Few K tiles, whose costs differ: an equal share of the cost would end in the
 // middle of most of them (148 alike, a few cheaper, on 148 CTAs: 332 us, and 210
 // one by one).  In the order of falling cost they go round the CTAs, to and fro.
-// All threads.
+// With fewer than LISTED_STEPS Q tiles per K tile, units of several K tiles save
+// more (480 K tiles, us with the attention: 1 Q tile each 47 one by one, 35 in
+// shares; 8: 92, 89; 10 to 15: 49, 52 and 102, 112).  All threads.
 __device__ __forceinline__ void deal_out(Tail &t, const Params &p) {
   const int total = t.listed, ctas = gridDim.x, x = blockIdx.x;
   for (int i = threadIdx.x; i < LISTED; i += THREADS) {
@@ -274,12 +277,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   if (warp == 0) {
     const int heads = p.c.Hkv / p.unit_heads;
-    int64_t run = 0, k_total = 0;
+    int64_t run = 0, k_total = 0, steps = 0;  // all K tiles; the Q tiles that they are multiplied with, at most
     for (int b = lane; b < p.c.B; b += 32)
-      if (t.seq[b].n > 0) k_total += static_cast<int64_t>(k_tiles(t.seq[b].L)) * heads;
+      if (t.seq[b].n > 0) {
+        const int64_t tiles = static_cast<int64_t>(k_tiles(t.seq[b].L)) * heads;
+        k_total += tiles;
+        steps += tiles * plan_windows(t.seq[b].n, p.tq);
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) k_total += __shfl_xor_sync(0xffffffffu, k_total, o);
-    const bool few = k_total <= ROUNDS * static_cast<int64_t>(gridDim.x) && k_total <= LISTED;
+    for (int o = 16; o > 0; o >>= 1) {
+      k_total += __shfl_xor_sync(0xffffffffu, k_total, o);
+      steps += __shfl_xor_sync(0xffffffffu, steps, o);
+    }
+    const bool few = k_total <= ROUNDS * static_cast<int64_t>(gridDim.x) && k_total <= LISTED &&
+                     steps >= LISTED_STEPS * k_total;
     for (int b0 = 0; b0 < p.c.B; b0 += 32) {
       const int b = b0 + lane;
       int64_t x = 0;
