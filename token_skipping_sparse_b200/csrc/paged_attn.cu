@@ -96,7 +96,7 @@ struct Item {
   int g;              // KV head
   int two;            // whether the window fills a second Q tile
   int t0, t1;         // key tiles
-  int a_end;          // with two Q tiles: end of those that the first one sees
+  int a_end;          // with two Q tiles: end of those that the first one goes over
   int whole;          // the piece is the unit
   int part;           // otherwise: place of its partial result
 };
@@ -230,7 +230,7 @@ __device__ __forceinline__ void walk(Tail &t, const Params &p) {
     it->two = w > p.tq && s.n - pc.p * w > p.tq;
     it->t0 = pc.t0;
     it->t1 = pc.t1;
-    it->a_end = (plan_visible(s, pc.p * w + p.tq) + BKV - 1) / BKV;
+    it->a_end = plan_first_end(s, shape_of(p), pc.p, pc.t0, pc.t1);
     it->whole = pc.whole;
     it->part = part;
     mbar_arrive(&t.item_full[count % ITEMS]);
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!it) break;
       const int t0 = uniform(it->t0), n = uniform(it->t1) - t0;
       const bool two = MODE != STEP && uniform(it->two) != 0;
-      // tiles of x = 0 when it has a Q tile of its own
+      // tiles of x = 0 when it has a Q tile of its own: at least one, if n is
       const int n_a = max(min(uniform(it->a_end) - t0, n), 0);
       give_back(item);
       if (n <= 0) continue;

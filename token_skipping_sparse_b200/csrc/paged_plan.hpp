@@ -87,6 +87,16 @@ SPTS_HD void plan_tiles(int off, int end, int c, int tiles, int &t0, int &t1) {
   t1 = end == c ? tiles : plan_min(tiles, (end + PLAN_TILE - 1) / PLAN_TILE);
 }
 
+// With two Q tiles: end of the key tiles that the first one goes over in the
+// piece [t0, t1) of window p.  Those it sees, and at least one of every piece that
+// has any: a warpgroup without a tile would have nothing to wait for, and run
+// ahead of the other one through the barrier that frees O.  (A tile that it does
+// not see is masked as a whole, and its rows stay as they are.)
+SPTS_HD int plan_first_end(const PlanSeq &s, PlanShape sh, int p, int t0, int t1) {
+  const int sees = (plan_visible(s, p * sh.w + sh.tile) + PLAN_TILE - 1) / PLAN_TILE;
+  return plan_min(t1, plan_max(sees, t0 + 1));
+}
+
 // Ranges a group of total cost `total` is cut into: none shorter than a tile.
 SPTS_HD int plan_ranges(int64_t total, int ctas) {
   const int64_t r = total / PLAN_TILE;
