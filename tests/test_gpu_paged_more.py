@@ -57,3 +57,46 @@ def test_more_new_tokens_than_cached_ones_in_head_groups():
     assert bool(((e[none:] - ref).abs() <= 2 * (err + 2.0 ** -21 * (1 + ref.abs()))).all())
     bound = 2 * (2 * T.U + 2 * err + 2.5e-4) * float(v.float().abs().max())
     assert bool(((o[none:].float() - want.float()).abs() <= bound).all())
+
+
+def test_two_streams_without_workspaces_of_the_callers():
+    # the same calls on two streams at once: attention in pieces, weights, eviction with the slots it keeps in between
+    cs = [T.Cache([1500 + 300 * i, 900], 16, 8, 128, seed=76 + i, spare=80) for i in range(2)]
+    qs = [T.packed([1 + 60 * i, 3], 32, 128, 78 + i) for i in range(2)]
+    cus = [T.i32(cu) for cu, _ in qs]
+    dst = [T.i32([c.free[:40], c.free[40:80]]) for c in cs]
+
+    def once(i):
+        w = torch.zeros(2, 8, cs[i].table.shape[1] * 16, device="cuda")
+        o = S.spts_paged_attention(qs[i][1], *cs[i].args(), cus[i], weights=w)
+        return (o, w) + S.spts_cache_evict(*cs[i].args(), w, 600, sink=4, recent=50, dst_table=dst[i], kept=True,
+                                           weights_out=torch.empty(2, 8, 640, device="cuda"))
+
+    ref = [once(i) for i in range(2)]
+    S.check_device_status()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(12):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].append(once(i))
+    torch.cuda.synchronize()
+    S.check_device_status()
+    for i in range(2):
+        assert all(torch.equal(x, y) for out in outs[i] for x, y in zip(out, ref[i]))
+
+
+def test_flags_of_calls_on_another_stream_are_found():
+    c = T.Cache([20], 16, 2, 64, seed=80)
+    cu, q = T.packed([1], 4, 64, 81)
+    bad, cu = T.i32([10 ** 6]), T.i32(cu)
+    S.check_device_status()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        S.spts_paged_attention(q, c.k, c.v, c.table, bad, cu)
+    side.synchronize()
+    with pytest.raises(S.SptsError):
+        S.check_device_status()
+    S.check_device_status()

@@ -222,8 +222,21 @@ def get_wait_limit_ns():
 
 
 def check_device_status(ws=None, stream=None):
-    ws = workspace(256) if ws is None else ws
-    check(lib.spts_check_device_status(ptr(ws), stream_ptr(stream)))
+    """Waits for the stream and raises what calls with this workspace have flagged; without one, what calls on the
+    current device with cached workspaces have (those on other streams as far as they have ended)."""
+    if ws is not None:
+        return check(lib.spts_check_device_status(ptr(ws), stream_ptr(stream)))
+    found = [workspace(256)]
+    with _ws_lock:
+        found += [t for (dev, _), t in _stream_ws.items() if dev == found[0].device]
+    failed = None
+    for t in found:  # all of them, so that no flag is left for a later call
+        try:
+            check(lib.spts_check_device_status(ptr(t), stream_ptr(stream)))
+        except SptsError as e:
+            failed = failed or e
+    if failed is not None:
+        raise failed
 
 
 def _attn_desc(dtype, Hq, Hkv, d, scale):
@@ -391,7 +404,9 @@ def spts_inject_salience(k, q_probe, rows, shift):
 # ---------------------------------------------------------------- the paged key/value cache
 # What the library cannot see behind a pointer (types, devices, strides) is
 # checked here: in one expression each, since a step of decoding is short, and
-# in words only once it has failed.
+# in words only once it has failed.  A call without `ws` uses a workspace that is
+# kept for its stream; a `ws` of your own must not serve two calls that may run at
+# once.
 _BF, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -488,15 +503,25 @@ def _scores(weights, cache, dev, what):
     return Hs, row, n
 
 
-def _own_ws(ws, nbytes, dev):
-    """The caller's workspace, or the cached one.  A captured graph would keep
-    the cached one's address after a larger call has replaced it."""
+_stream_ws = {}  # (device, stream): the workspace of the calls below that are given none
+
+
+def _own_ws(ws, nbytes, dev, stream):
+    """The caller's workspace, or the one cached for the stream: calls on
+    different streams may run at once.  It is allocated on that stream, so what
+    a larger one replaces is free for others only behind the calls that use it.
+    A captured graph would keep its address after that."""
     if ws is not None:
         return _want(ws, torch.uint8, 1, dev, "ws")
     if _capturing():
         raise ValueError("pass a workspace of your own (ws) while a graph is captured")
-    t = _ws_cache.get(dev)
-    return t if t is not None and t.numel() >= nbytes else workspace(nbytes, dev)
+    t = _stream_ws.get((dev, stream))
+    if t is None or t.numel() < nbytes:
+        with _ws_lock:
+            t = _stream_ws.get((dev, stream))
+            if t is None or t.numel() < nbytes:
+                t = _stream_ws[dev, stream] = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+    return t
 
 
 def _elsewhere(dev, who):
@@ -531,9 +556,10 @@ def spts_cache_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, cu_n
     if v_new.shape != shape or Hkv != heads or d != dim:
         raise ValueError("k_new, v_new and the pages must agree in tokens, heads and head dim")
     cu, at = _vector(cu_new, B + 1, dev, "cu_new"), None if pos is None else _vector(pos, T, dev, "pos")
-    ws = _own_ws(ws, 256, dev)
+    stream = _raw_stream(dev.index)
+    ws = _own_ws(ws, 256, dev, stream)
     check(lib.spts_cache_append(C.byref(_bf16_desc(Hkv, Hkv, d)), cache, k_new.data_ptr(), k_stride,
-                                v_new.data_ptr(), v_stride, cu, T, at, theta, ws.data_ptr(), _raw_stream(dev.index)))
+                                v_new.data_ptr(), v_stride, cu, T, at, theta, ws.data_ptr(), stream))
 
 
 def spts_paged_attention_workspace(q, k_pages, v_pages, page_table, seq_lens, weights=False):
@@ -569,12 +595,13 @@ def spts_paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_q, scale=
         Hs, stride, n = _scores(weights, cache, dev, "weights")
         if n < max_pages * page:
             raise ValueError("weights: need a slot for every slot of a page table row")
-    ws = _own_ws(ws, _attention_ws_bytes(Hq, Hkv, d, B, page, max_pages, T, 0 if weights is None else 1), dev)
+    stream = _raw_stream(dev.index)
+    ws = _own_ws(ws, _attention_ws_bytes(Hq, Hkv, d, B, page, max_pages, T, 0 if weights is None else 1), dev, stream)
     a = _bf16_desc(Hq, Hkv, d, 0.0 if scale is None else float(scale))
     check(lib.spts_paged_attention(C.byref(a), view, q.data_ptr(), q_stride, _vector(cu_q, B + 1, dev, "cu_q"), T,
                                    o.data_ptr(), o_stride, None if e is None else e.data_ptr(),
                                    None if weights is None else weights.data_ptr(), Hs, stride, ws.data_ptr(),
-                                   ws.numel(), _raw_stream(dev.index)))
+                                   ws.numel(), stream))
     return (o, e) if lse else o
 
 
@@ -610,12 +637,12 @@ def spts_cache_evict(k_pages, v_pages, page_table, seq_lens, weights, keep, sink
     if new_lens is None:
         new_lens = seq_lens.new_empty(B)
     idx = seq_lens.new_empty((B, Hs, keep)) if kept else None
-    ws = _own_ws(ws, lib.spts_cache_evict_workspace(view, Hs, keep), dev)
+    stream = _raw_stream(dev.index)
+    ws = _own_ws(ws, lib.spts_cache_evict_workspace(view, Hs, keep), dev, stream)
     check(lib.spts_cache_evict(C.byref(_bf16_desc(Hkv, Hkv, d)), view, weights.data_ptr(), Hs, stride, keep, sink,
                                recent, dst.data_ptr(), dst.shape[1], _table_stride(dst, "dst_table"),
                                weights_out.data_ptr(), out_stride, _vector(new_lens, B, dev, "new_lens"),
-                               None if idx is None else idx.data_ptr(), ws.data_ptr(), ws.numel(),
-                               _raw_stream(dev.index)))
+                               None if idx is None else idx.data_ptr(), ws.data_ptr(), ws.numel(), stream))
     return (new_lens, weights_out, idx) if kept else (new_lens, weights_out)
 
 
