@@ -17,6 +17,7 @@ SHIM = plan_tests.SHIM + r"""
 extern "C" int first_end(int n, int L, int w, int tile, int p, int t0, int t1) {
   return plan_first_end(PlanSeq{n, L}, PlanShape{w, tile}, p, t0, t1);
 }
+extern "C" int has_slot(int t, int max_pages, int page_shift) { return paged_has_slot(t, max_pages, page_shift); }
 """
 
 
@@ -176,3 +177,11 @@ def test_every_warpgroup_has_a_tile_of_every_piece(plan):
                 end = plan.first_end(n, L, 64, 32, p, t0, t1)
                 assert t0 < end <= t1 and end >= min(-(-first // 128), t1)
             assert plan.first_end(n, L, 64, 32, p, tiles, tiles) == tiles
+
+
+def test_only_slots_of_a_table_row_are_slots(plan):
+    for shift in (4, 8):
+        for pages in (1, 3, 1 << 18):
+            cap = pages << shift
+            for t, ok in ((0, 1), (cap - 1, 1), (cap, 0), (cap + 1, 0), (-1, 0), (2 ** 31 - 1, 0), (-2 ** 31, 0)):
+                assert bool(plan.has_slot(t, pages, shift)) == bool(ok), (t, pages, shift)

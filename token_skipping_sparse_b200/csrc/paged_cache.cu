@@ -4,6 +4,7 @@
 // to speak of.
 #include "host.hpp"
 #include "paged.cuh"
+#include "paged_plan.hpp"
 #include "rowops.cuh"
 #include "sm100.cuh"
 
@@ -263,9 +264,14 @@ __device__ __forceinline__ int64_t dst_offset(const PagedView &c, const EvictArg
   const int page = paged_page(e.dst_table, e.dst_stride, c.num_pages, b, entry, e.status);
   return page < 0 ? -1 : paged_offset(c, page, t, g);
 }
+// The kept slots come from the caller's workspace: one that is none (two calls
+// at once with one workspace) is flagged, and nothing is read outside the rows.
 __device__ __forceinline__ int64_t src_offset(const PagedView &c, const EvictArgs &e, int b, int from, int g) {
-  const int page = from < 0 ? -1
-                            : paged_page(c.table, c.table_stride, c.num_pages, b, from >> c.page_shift, e.status);
+  if (!paged_has_slot(from, c.max_pages, c.page_shift)) {
+    raise_status(e.status, SPTS_DEV_BADINDEX, kSiteSlot, static_cast<uint32_t>(from));
+    return -1;
+  }
+  const int page = paged_page(c.table, c.table_stride, c.num_pages, b, from >> c.page_shift, e.status);
   return page < 0 ? -1 : paged_offset(c, page, from, g);
 }
 
@@ -275,18 +281,20 @@ constexpr int COPY_ROWS = 128;  // rows of a CTA
 
 // The weights of one row's kept tokens, then zeros; in place too: a tile of
 // TILE entries is read before it is written, kept[t] >= t and ascending, so a
-// tile's writes never reach the source of a later one.
-__device__ __forceinline__ void move_weights(const EvictArgs &e, int row, int n) {
+// tile's writes never reach the source of a later one.  A slot that is none is
+// flagged where its row is moved.
+__device__ __forceinline__ void move_weights(const PagedView &c, const EvictArgs &e, int row, int n) {
   constexpr int U = 16, TILE = U * MOVE_THREADS;
   const float *w = e.weights + row * e.w_stride;
   const int32_t *kept = e.kept + row * e.kept_stride;
   float *out = e.weights_out + row * e.w_out_stride;
+  const uint32_t last = (static_cast<uint32_t>(c.max_pages) << c.page_shift) - 1;
   for (int base = 0; base < n; base += TILE) {
     float v[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int t = base + u * MOVE_THREADS + threadIdx.x;
-      if (t < n) v[u] = w[kept[t]];
+      if (t < n) v[u] = w[min(static_cast<uint32_t>(kept[t]), last)];
     }
     __syncthreads();
 #pragma unroll
@@ -311,7 +319,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_copy_kernel(PagedView c, E
   const int n = min(paged_len(c, b, nullptr), e.keep);
   if (part == parts) {
     if (g == 0 && threadIdx.x == 0) e.new_lens[b] = n;
-    if (g < e.Hs) move_weights(e, b * e.Hs + g, n);
+    if (g < e.Hs) move_weights(c, e, b * e.Hs + g, n);
     return;
   }
   const int base = part * COPY_ROWS, rows = min(n - base, COPY_ROWS);
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(SHIFT_THREADS) evict_shift_kernel(PagedView c,
 
 __global__ void __launch_bounds__(MOVE_THREADS) evict_weights_kernel(PagedView c, EvictArgs e) {
   const int row = blockIdx.x;
-  move_weights(e, row, min(paged_len(c, row / e.Hs, nullptr), e.keep));
+  move_weights(c, e, row, min(paged_len(c, row / e.Hs, nullptr), e.keep));
 }
 
 // The frequencies of the last (d, theta) of this thread: 64 powers cost more

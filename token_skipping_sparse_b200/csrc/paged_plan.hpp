@@ -37,6 +37,11 @@ constexpr int PLAN_ONE = SPTS_PLAN_ONE, PLAN_TWO = SPTS_PLAN_TWO;
 SPTS_HD int plan_min(int a, int b) { return a < b ? a : b; }
 SPTS_HD int plan_max(int a, int b) { return a > b ? a : b; }
 
+// Whether a row of a page table has a slot t.
+SPTS_HD bool paged_has_slot(int t, int max_pages, int page_shift) {
+  return t >= 0 && (t >> page_shift) < max_pages;
+}
+
 struct PlanShape {
   int w, tile;  // tokens of a window (one or two Q tiles) and of a Q tile
 };
