@@ -100,3 +100,19 @@ def test_flags_of_calls_on_another_stream_are_found():
     with pytest.raises(S.SptsError):
         S.check_device_status()
     S.check_device_status()
+
+
+@pytest.mark.parametrize("each", [True, False])
+def test_evict_to_a_table_just_wide_enough_for_the_lengths(each):
+    # every sequence is shorter than the budget, and so is a row of the destination
+    lens, Hkv, d, page, keep = [1000, 17, 300], 2, 64, 16, 2048
+    c = T.Cache(lens, page, Hkv, d, seed=82, spare=200)
+    T.widen(c, 8192)
+    w = T.weights_of(c, Hkv if each else 1, 83, "spread")
+    dst = [[c.free.pop() if i * page < n else -1 for i in range(63)] for n in lens]
+    want = P.cache_evict(c.np_k, c.np_v, c.rows, lens, T.f64(w), keep, 4, 100, dst, keep)
+    new_lens, w_out, kept = S.spts_cache_evict(*c.args(), w, keep, sink=4, recent=100, dst_table=T.i32(dst), kept=True)
+    S.check_device_status()
+    assert new_lens.tolist() == lens and np.array_equal(kept.cpu().numpy(), want[4])
+    assert np.array_equal(T.f64(w_out), want[2])
+    assert np.array_equal(T.f64(c.k), want[0], equal_nan=True) and np.array_equal(T.f64(c.v), want[1], equal_nan=True)

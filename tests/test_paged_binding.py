@@ -31,3 +31,41 @@ def test_a_workspace_that_is_given_is_used(eager):
     ws = torch.zeros(512, dtype=torch.uint8)
     assert S._lib._own_ws(ws, 256, CPU, 7) is ws
     assert not S._lib._stream_ws
+
+
+class Calls:
+    """In the library's place: sizes from it, launches written down."""
+
+    def __init__(self):
+        self.seen = []
+
+    def __getattr__(self, name):
+        real = getattr(S.lib, name)
+        if name.endswith("_workspace"):
+            return real
+
+        def call(*args):
+            self.seen.append((name,) + args)
+            return S.OK
+        return call
+
+
+@pytest.fixture
+def host(eager):
+    """Calls with tensors on the host, as far as the library."""
+    calls = Calls()
+    eager.setattr(S._lib, "lib", calls)
+    eager.setattr(S._lib, "_elsewhere", lambda dev, who: False)
+    eager.setattr(S._lib, "_raw_stream", lambda index: 7)
+    eager.setattr(S._lib, "_vector", lambda t, n, dev, what: t.data_ptr())
+    return calls
+
+
+def test_weights_out_has_room_for_the_budget(host):
+    k = torch.zeros(600, 16, 2, 64, dtype=torch.bfloat16)
+    table, lens = torch.zeros(1, 512, dtype=torch.int32), torch.tensor([1000], dtype=torch.int32)
+    w = torch.zeros(1, 2, 8192)
+    for keep, width, columns in ((2048, 63, 2048), (1008, 63, 1008), (500, 63, 1008), (9000, 63, 8192)):
+        _, out = S._lib.spts_cache_evict(k, k.clone(), table, lens, w, keep,
+                                         dst_table=torch.zeros(1, width, dtype=torch.int32))
+        assert out.shape == (1, 2, columns), (keep, width)

@@ -630,7 +630,8 @@ def spts_cache_evict(k_pages, v_pages, page_table, seq_lens, weights, keep, sink
     if dst.shape[0] != B:
         raise ValueError("dst_table: need one row per sequence")
     if weights_out is None:
-        weights_out = weights if dst_table is None else weights.new_empty((B, Hs, dst.shape[1] * page))
+        width = max(dst.shape[1] * page, min(keep, max_pages * page))
+        weights_out = weights if dst_table is None else weights.new_empty((B, Hs, width))
     Ho, out_stride, m = _scores(weights_out, cache, dev, "weights_out")
     if Ho != Hs or m != out_stride:
         raise ValueError("weights_out: need contiguous rows, as many as weights has")
