@@ -116,3 +116,20 @@ def test_evict_to_a_table_just_wide_enough_for_the_lengths(each):
     assert new_lens.tolist() == lens and np.array_equal(kept.cpu().numpy(), want[4])
     assert np.array_equal(T.f64(w_out), want[2])
     assert np.array_equal(T.f64(c.k), want[0], equal_nan=True) and np.array_equal(T.f64(c.v), want[1], equal_nan=True)
+
+
+@pytest.mark.parametrize("lens", [[300], [300, 41]])
+def test_evict_to_the_first_columns_of_the_own_table(lens):
+    # a view of the page table starts where the table does: the rows move in place, the weights to a row of their own
+    page, keep = 16, 60
+    c = T.Cache(lens, page, 2, 64, seed=84)
+    w = T.weights_of(c, 2, 85, "spread")
+    view = c.table[:, :4]
+    want = P.cache_evict(c.np_k, c.np_v, c.rows, lens, T.f64(w), keep, 2, 9, c.rows, 64)
+    new_lens, w_out, kept = S.spts_cache_evict(*c.args(), w, keep, sink=2, recent=9, dst_table=view, kept=True)
+    S.check_device_status()
+    assert new_lens.tolist() == want[3] and np.array_equal(kept.cpu().numpy(), want[4])
+    assert np.array_equal(T.f64(w_out), want[2])
+    for b, n in enumerate(want[3]):
+        p, r = P.slot_rows(c.rows[b], n, page)
+        assert np.array_equal(T.f64(c.k)[p, r], want[0][p, r]) and np.array_equal(T.f64(c.v)[p, r], want[1][p, r])

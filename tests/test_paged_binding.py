@@ -69,3 +69,15 @@ def test_weights_out_has_room_for_the_budget(host):
         _, out = S._lib.spts_cache_evict(k, k.clone(), table, lens, w, keep,
                                          dst_table=torch.zeros(1, width, dtype=torch.int32))
         assert out.shape == (1, 2, columns), (keep, width)
+
+
+def test_the_first_columns_of_one_sequences_own_table_are_that_table():
+    # one row has no stride: nothing but the workspace is missing here
+    a = S._lib.AttnDesc(S.BF16, 4, 2, 64, 0.0)
+
+    def status(B, dst_stride):
+        c = S._lib.PagedCache(0x100000, 0x200000, 100, 0, 16, B, 0x300000, 8, 0, 0x400000)
+        return S.lib.spts_cache_evict(S._lib.C.byref(a), S._lib.C.byref(c), 0x500000, 2, 128, 20, 0, 0, 0x300000, 4,
+                                      dst_stride, 0x600000, 128, 0x700000, None, None, 0, None)
+    assert status(1, 4) == S.ERR_WORKSPACE and status(1, 8) == S.ERR_WORKSPACE
+    assert status(2, 4) == S.ERR_SHAPE and status(2, 8) == S.ERR_WORKSPACE

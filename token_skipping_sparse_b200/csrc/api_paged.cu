@@ -189,7 +189,7 @@ spts_status spts_cache_evict(const spts_attn_desc *a, const spts_paged_cache *c,
   if (dst_stride == 0) dst_stride = dst_max_pages;
   SPTS_REQUIRE(dst_max_pages >= 1 && (dst_stride >= dst_max_pages || c->B == 1), SPTS_ERR_SHAPE,
                "%s: need dst_max_pages >= 1 and dst_stride >= dst_max_pages", who);
-  SPTS_REQUIRE(dst_table != c->page_table || dst_stride == view.table_stride, SPTS_ERR_SHAPE,
+  SPTS_REQUIRE(dst_table != c->page_table || dst_stride == view.table_stride || c->B == 1, SPTS_ERR_SHAPE,
                "%s: dst_table is page_table, but the strides differ", who);
   SPTS_TRY(check_ws(ws, ws_bytes, spts_cache_evict_workspace(c, Hs, keep), who));
   Carver cv(ws, ws_bytes);
