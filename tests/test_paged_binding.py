@@ -81,3 +81,9 @@ def test_the_first_columns_of_one_sequences_own_table_are_that_table():
                                       dst_stride, 0x600000, 128, 0x700000, None, None, 0, None)
     assert status(1, 4) == S.ERR_WORKSPACE and status(1, 8) == S.ERR_WORKSPACE
     assert status(2, 4) == S.ERR_SHAPE and status(2, 8) == S.ERR_WORKSPACE
+
+
+def test_a_workspace_with_fewer_bytes_than_entries_is_refused(eager):
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(4096), torch.zeros(4096, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            S._lib._own_ws(bad, 256, CPU, 7)

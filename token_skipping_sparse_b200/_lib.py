@@ -512,7 +512,9 @@ def _own_ws(ws, nbytes, dev, stream):
     a larger one replaces is free for others only behind the calls that use it.
     A captured graph would keep its address after that."""
     if ws is not None:
-        return _want(ws, torch.uint8, 1, dev, "ws")
+        if not _want(ws, torch.uint8, 1, dev, "ws").is_contiguous():
+            raise ValueError("ws: need contiguous bytes")
+        return ws
     if _capturing():
         raise ValueError("pass a workspace of your own (ws) while a graph is captured")
     t = _stream_ws.get((dev, stream))
