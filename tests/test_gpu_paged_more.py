@@ -133,3 +133,45 @@ def test_evict_to_the_first_columns_of_the_own_table(lens):
     for b, n in enumerate(want[3]):
         p, r = P.slot_rows(c.rows[b], n, page)
         assert np.array_equal(T.f64(c.k)[p, r], want[0][p, r]) and np.array_equal(T.f64(c.v)[p, r], want[1][p, r])
+
+
+def check_long_sums(B, n, Hq, Hkv, d, each, width=None):
+    """n new tokens of the first of B sequences, nothing else cached; K is 0 at the first ten slots and far off at all
+    others, so that row i gives 1 / min(i + 1, 10) to each of the first min(i + 1, 10) slots, for every head.
+
+    The scores are 0, or below the exponential's range.  Each weight is off by 2^-19 of itself (exp2, normaliser: the
+    same for all rows), and the sum of a slot's by what is rounded outside of the compensated sum: 32 additions inside
+    a block of rows, 2 more and 2 of the compensation, 3 for the shares of four warps, Hkv over the heads and one for
+    what was there: not by their number.
+    """
+    page = 128
+    n_pages = -(-n // page)
+    k = torch.full((n_pages, page, Hkv, d), -16.0, dtype=torch.bfloat16, device="cuda")
+    k.view(-1, Hkv, d)[:10] = 0
+    v = torch.randn(n_pages, page, Hkv, d, device="cuda").bfloat16()
+    q = torch.ones(n, Hq, d, dtype=torch.bfloat16, device="cuda")
+    table = torch.full((B, width or n_pages), -1, dtype=I32, device="cuda")
+    table[0, :n_pages] = torch.arange(n_pages)
+    w = torch.zeros(B, Hkv if each else 1, table.shape[1] * page, device="cuda")
+    cu = [0] + [n] * B
+    S.spts_paged_attention(q, k, v, table, T.i32([n] + [0] * (B - 1)), T.i32(cu), weights=w)
+    S.check_device_status()
+    rows = 1 / np.minimum(np.arange(n) + 1.0, 10)
+    want = np.array([rows[j:].sum() for j in range(10)]) * (Hq // Hkv if each else Hq)
+    got = T.f64(w[0])
+    bound = (2.0 ** -19 + (32 + 2 + 2 + 3 + Hkv + 1) * 2.0 ** -24) * want
+    assert np.all(np.abs(got[:, :10] - want) <= bound), np.abs(got[:, :10] / want - 1).max()
+    assert not got[:, 10:].any() and not w[1:].any()
+
+
+@pytest.mark.parametrize("each,width", [(True, None), (False, None), (False, 16500)])
+def test_weights_of_many_rows_are_sums_of_all_of_them(each, width):
+    # a wide table (16500 x 128 slots x 8 heads of fp32: above the room for sums per head): a unit walks all heads itself
+    check_long_sums(1, 8192, 32, 8, 64, each, width)
+
+
+@pytest.mark.parametrize("B", [256, 1024])
+@pytest.mark.parametrize("each", [True, False])
+def test_stored_weights_of_many_rows_are_sums_of_all_of_them(each, B):
+    # few rows per sequence on average, all of them one sequence's: the attention leaves the scores (134 MB)
+    check_long_sums(B, 1024, 32, 8, 128, each)

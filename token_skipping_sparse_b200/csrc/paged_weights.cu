@@ -13,6 +13,8 @@
 // two K tiles the warpgroups share out the Q tiles instead, and their sums are
 // added in order at the end: 7
 // sequences of 685 new tokens in 738, 2 heads of 8 (84 K tiles), 68 -> 46 us.
+// The sums over the Q tiles keep what they round away (LongSum): with 8 x 4 heads
+// a prompt of 8192 rows adds 2048 tiles to a slot's weight over all heads.
 // Bound by the
 // exponentials (16384 per K and Q tile: 1024 cycles of the MUFU pipe against
 // 512 of the MMA) when there are many rows, by reading K when there are few.
@@ -96,6 +98,18 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// A sum of many parts that keeps what each addition rounds away (Kahan 1965): as
+// good as one rounding, however many.  Added one by one in fp32, 16384 weights of
+// 0.1 are off by 1.5e-4 of their sum, and small ones behind large ones are lost.
+struct LongSum {
+  float sum, lost;
+  __device__ __forceinline__ void add(float part) {
+    const float y = part - lost, s = sum + y;
+    lost = (s - sum) - y;
+    sum = s;
+  }
+};
 
 __device__ __forceinline__ int k_tiles(int L) { return (L + BKV - 1) / BKV; }
 
@@ -478,7 +492,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float l = __ldg(p.lse + static_cast<int64_t>(first + tok) * p.Hq + (g0 + h) * p.G + rh);
         return l == -INFINITY ? 0.f : -LOG2E * l;  // a row that sees nothing: every column of it is masked
       };
-      float next = lse_of(0, q0), sum[4] = {0.f, 0.f, 0.f, 0.f};
+      float next = lse_of(0, q0);
+      LongSum tiles_sum{};  // over the Q tiles; inside one, four sums of 32
       for (int h = 0; ok && h < p.unit_heads; ++h) {
         for (int q = q0; q < q1; q += share, ++sc) {
           uint64_t *lse_full = &t.lse_full[2 * wg + (sc & 1)];
@@ -494,6 +509,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int lo = (slot - base - q * p.tq) * p.G, hi = min(p.tq, n - q * p.tq) * p.G;
           const bool early = __any_sync(0xffffffffu, lo > 0);  // some slot of this warp is behind some row
           const float4 *ls = reinterpret_cast<const float4 *>(t.lse[wg][sc & 1]);
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t xr[64];
@@ -525,10 +541,11 @@ __global__ void __launch_bounds__(THREADS, 1)
               sum[3] += ex2(fmaf(__uint_as_float(xr[4 * e + 3]), c2, l4.w));
             }
           }
+          tiles_sum.add((sum[0] + sum[1]) + (sum[2] + sum[3]));
         }
       }
       if (!ok) break;
-      float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float total = tiles_sum.sum;
       if (part > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(&t.join_free[wg], ((joined >> wg) & 1u) ^ 1u, abort_flag, p.status,
                                                p.wait_ns, 0x68u));
@@ -578,6 +595,9 @@ __global__ void __launch_bounds__(256) paged_weights_sum_kernel(PagedView c, con
 // the chain of loads where a slot has many rows (up to 20 rows of 4 heads over
 // 438 slots: the whole call 28 us against 43).
 constexpr int STORED_WARPS = 4;
+// More weights than this of a warp go to long sums, block by block (always doing so took registers: 16 rows of 8 x 4
+// heads, the whole call 70.9 us against 70.0; 69.4 without any).
+constexpr int STORED_BLOCK = 32;
 
 __global__ void __launch_bounds__(32 * STORED_WARPS)
     stored_weights_kernel(PagedView c, const int32_t *__restrict__ cu, int T, int Hq, float scale_log2,
@@ -594,23 +614,42 @@ __global__ void __launch_bounds__(32 * STORED_WARPS)
   const int heads = Hq / Hs, base = L - n;
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
   int i = warp / heads, h = warp % heads;  // row and head
+  int e = warp;
+  auto add_rows = [&](int end) {
 #pragma unroll 4
-  for (int e = warp; e < n * heads; e += STORED_WARPS) {
-    const int64_t row = static_cast<int64_t>(first + i) * Hq + hs * heads + h;
-    const int seen = base + i - slot;  // the row sees slots 0..seen of the four
-    if (slot < L && seen >= 0) {
-      const float4 s = *reinterpret_cast<const float4 *>(scores + row * score_stride + slot);
-      const float l = -LOG2E * lse[row];
-      sum[0] += ex2(fmaf(s.x, scale_log2, l));
-      if (seen >= 1) sum[1] += ex2(fmaf(s.y, scale_log2, l));
-      if (seen >= 2) sum[2] += ex2(fmaf(s.z, scale_log2, l));
-      if (seen >= 3) sum[3] += ex2(fmaf(s.w, scale_log2, l));
+    for (; e < end; e += STORED_WARPS) {
+      const int64_t row = static_cast<int64_t>(first + i) * Hq + hs * heads + h;
+      const int seen = base + i - slot;  // the row sees slots 0..seen of the four
+      if (slot < L && seen >= 0) {
+        const float4 s = *reinterpret_cast<const float4 *>(scores + row * score_stride + slot);
+        const float l = -LOG2E * lse[row];
+        sum[0] += ex2(fmaf(s.x, scale_log2, l));
+        if (seen >= 1) sum[1] += ex2(fmaf(s.y, scale_log2, l));
+        if (seen >= 2) sum[2] += ex2(fmaf(s.z, scale_log2, l));
+        if (seen >= 3) sum[3] += ex2(fmaf(s.w, scale_log2, l));
+      }
+      h += STORED_WARPS;
+      while (h >= heads) {
+        h -= heads;
+        ++i;
+      }
     }
-    h += STORED_WARPS;
-    while (h >= heads) {
-      h -= heads;
-      ++i;
+  };
+  const int rows = n * heads;
+  if (rows <= STORED_BLOCK * STORED_WARPS) {
+    add_rows(rows);
+  } else {
+    LongSum total[4]{};
+    while (e < rows) {
+      add_rows(min(rows, e + STORED_BLOCK * STORED_WARPS));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        total[k].add(sum[k]);
+        sum[k] = 0.f;
+      }
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[k] = total[k].sum;
   }
   sums[warp][lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
   __syncthreads();
