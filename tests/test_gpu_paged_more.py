@@ -175,3 +175,45 @@ def test_weights_of_many_rows_are_sums_of_all_of_them(each, width):
 def test_stored_weights_of_many_rows_are_sums_of_all_of_them(each, B):
     # few rows per sequence on average, all of them one sequence's: the attention leaves the scores (134 MB)
     check_long_sums(B, 1024, 32, 8, 128, each)
+
+
+STEPS = {
+    # new tokens of each sequence, earlier ones; one token each or less on average
+    "steps": ([1] * 9, [0, 1, 15, 16, 127, 128, 300, 129, 511]),
+    "some without a token": ([1, 0, 1, 0, 1, 1], [40, 200, 130, 0, 0, 255]),
+    "one with several": ([5, 0, 0, 1, 0, 0, 1, 0], [130, 9, 0, 260, 40, 3, 0, 0]),
+}
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("name", STEPS)
+@pytest.mark.parametrize("G,Hkv,d", [(3, 2, 128), (5, 2, 64), (7, 1, 128), (7, 2, 64), (8, 2, 128), (16, 1, 128),
+                                     (16, 2, 64)])
+def test_steps_of_every_group_width(G, Hkv, d, name, wide):
+    # Q tiles of 16 rows with and without padding rows, windows of one token (8 and 16 heads to a group) and of more
+    new, old = STEPS[name]
+    c = T.Cache([n + o for n, o in zip(new, old)], 16, Hkv, d, seed=90 + G)
+    if wide:
+        T.widen(c)
+    T.check_attention(c, new, G * Hkv, Hkv, d, seed=91, lse=False)
+    T.check_attention(c, new, G * Hkv, Hkv, d, seed=92)
+    for each in (True, False):
+        T.check_attention(c, new, G * Hkv, Hkv, d, seed=93, each=each)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("G,Hkv,d", [(1, 2, 128), (2, 2, 64), (3, 2, 128), (3, 1, 64), (5, 1, 128), (7, 2, 64)])
+def test_few_rows_of_every_group_width(G, Hkv, d, wide):
+    # up to 16 rows of a KV head per sequence on average: one to three tokens, and one sequence with more than a Q tile
+    many = 128 // G + 3
+    few = [1, 2, 3, 1] * 40
+    count = next(k for k in range(2, 160) if (many + sum(few[:k])) * G <= 16 * (k + 1) and many + sum(few[:k]) > k + 1)
+    new = [many] + few[:count]
+    assert sum(new) > len(new) and sum(new) * G <= 16 * len(new)
+    lens = [n + (37 * i) % 290 for i, n in enumerate(new)]
+    c = T.Cache(lens, 32, Hkv, d, seed=94 + G)
+    if wide:
+        T.widen(c)
+    T.check_attention(c, new, G * Hkv, Hkv, d, seed=95, lse=False)
+    for each in (True, False):
+        T.check_attention(c, new, G * Hkv, Hkv, d, seed=96, each=each)
