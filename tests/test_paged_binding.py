@@ -1,5 +1,8 @@
 """The binding of the paged key/value cache, as far as it runs without a GPU."""
 
+import threading
+import time
+
 import pytest
 import torch
 
@@ -87,3 +90,35 @@ def test_a_workspace_with_fewer_bytes_than_entries_is_refused(eager):
     for bad in (torch.zeros(1, dtype=torch.uint8).expand(4096), torch.zeros(4096, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError, match="contiguous"):
             S._lib._own_ws(bad, 256, CPU, 7)
+
+
+@pytest.mark.parametrize("own", [False, True])
+def test_kernels_of_two_threads_do_not_mix_in_one_workspace(host, own):
+    # a call that is given no workspace launches all its kernels before another one does
+    inside, most = [], []
+
+    def launch(*args):
+        inside.append(args[-2])
+        most.append(len(inside))
+        time.sleep(0.02)
+        inside.pop()
+        return S.OK
+    for name in ("spts_cache_append", "spts_paged_attention", "spts_cache_evict"):
+        setattr(host, name, launch)
+    k = torch.zeros(8, 16, 2, 64, dtype=torch.bfloat16)
+    table, lens, cu = torch.arange(8, dtype=torch.int32)[None], torch.tensor([40], dtype=torch.int32), \
+        torch.tensor([0, 3], dtype=torch.int32)
+    rows, w = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 2, 128)
+
+    def calls():
+        ws = torch.zeros(1 << 22, dtype=torch.uint8) if own else None
+        for _ in range(3):
+            S._lib.spts_cache_append(rows, rows, k, k.clone(), table, lens, cu, ws=ws)
+            S._lib.spts_paged_attention(rows, k, k.clone(), table, lens, cu, weights=w, ws=ws)
+            S._lib.spts_cache_evict(k, k.clone(), table, lens, w, 20, ws=ws)
+    threads = [threading.Thread(target=calls) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(most) == 27 and (max(most) > 1) == own

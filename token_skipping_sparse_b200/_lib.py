@@ -9,6 +9,7 @@ arithmetic runs in the library's CUDA kernels; there is no fallback path.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import functools
 import os
@@ -228,7 +229,7 @@ def check_device_status(ws=None, stream=None):
         return check(lib.spts_check_device_status(ptr(ws), stream_ptr(stream)))
     found = [workspace(256)]
     with _ws_lock:
-        found += [t for (dev, _), t in _stream_ws.items() if dev == found[0].device]
+        found += [t for (dev, _), t in _stream_ws.items() if dev == found[0].device.index]
     failed = None
     for t in found:  # all of them, so that no flag is left for a later call
         try:
@@ -503,7 +504,11 @@ def _scores(weights, cache, dev, what):
     return Hs, row, n
 
 
-_stream_ws = {}  # (device, stream): the workspace of the calls below that are given none
+_stream_ws = {}  # (device index, stream): the workspace of the calls below that are given none
+# A call launches several kernels: those of two threads on one stream must not
+# mix while both use the stream's workspace.
+_issue_lock = threading.Lock()
+_no_lock = contextlib.nullcontext()
 
 
 def _own_ws(ws, nbytes, dev, stream):
@@ -517,12 +522,13 @@ def _own_ws(ws, nbytes, dev, stream):
         return ws
     if _capturing():
         raise ValueError("pass a workspace of your own (ws) while a graph is captured")
-    t = _stream_ws.get((dev, stream))
+    key = dev.index, stream
+    t = _stream_ws.get(key)
     if t is None or t.numel() < nbytes:
         with _ws_lock:
-            t = _stream_ws.get((dev, stream))
+            t = _stream_ws.get(key)
             if t is None or t.numel() < nbytes:
-                t = _stream_ws[dev, stream] = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+                t = _stream_ws[key] = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
     return t
 
 
@@ -559,9 +565,11 @@ def spts_cache_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, cu_n
         raise ValueError("k_new, v_new and the pages must agree in tokens, heads and head dim")
     cu, at = _vector(cu_new, B + 1, dev, "cu_new"), None if pos is None else _vector(pos, T, dev, "pos")
     stream = _raw_stream(dev.index)
+    lock = _issue_lock if ws is None else _no_lock
     ws = _own_ws(ws, 256, dev, stream)
-    check(lib.spts_cache_append(C.byref(_bf16_desc(Hkv, Hkv, d)), cache, k_new.data_ptr(), k_stride,
-                                v_new.data_ptr(), v_stride, cu, T, at, theta, ws.data_ptr(), stream))
+    with lock:
+        check(lib.spts_cache_append(C.byref(_bf16_desc(Hkv, Hkv, d)), cache, k_new.data_ptr(), k_stride,
+                                    v_new.data_ptr(), v_stride, cu, T, at, theta, ws.data_ptr(), stream))
 
 
 def spts_paged_attention_workspace(q, k_pages, v_pages, page_table, seq_lens, weights=False):
@@ -592,18 +600,21 @@ def spts_paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_q, scale=
         if o.shape != shape:
             raise ValueError("out: need q's shape")
     e = q.new_empty((T, Hq), dtype=_F32) if lse else None
-    Hs = stride = 0
+    Hs = w_stride = 0
     if weights is not None:
-        Hs, stride, n = _scores(weights, cache, dev, "weights")
+        Hs, w_stride, n = _scores(weights, cache, dev, "weights")
         if n < max_pages * page:
             raise ValueError("weights: need a slot for every slot of a page table row")
     stream = _raw_stream(dev.index)
+    lock = _issue_lock if ws is None else _no_lock
     ws = _own_ws(ws, _attention_ws_bytes(Hq, Hkv, d, B, page, max_pages, T, 0 if weights is None else 1), dev, stream)
     a = _bf16_desc(Hq, Hkv, d, 0.0 if scale is None else float(scale))
-    check(lib.spts_paged_attention(C.byref(a), view, q.data_ptr(), q_stride, _vector(cu_q, B + 1, dev, "cu_q"), T,
-                                   o.data_ptr(), o_stride, None if e is None else e.data_ptr(),
-                                   None if weights is None else weights.data_ptr(), Hs, stride, ws.data_ptr(),
-                                   ws.numel(), stream))
+    cu = _vector(cu_q, B + 1, dev, "cu_q")
+    with lock:
+        check(lib.spts_paged_attention(C.byref(a), view, q.data_ptr(), q_stride, cu, T, o.data_ptr(), o_stride,
+                                       None if e is None else e.data_ptr(),
+                                       None if weights is None else weights.data_ptr(), Hs, w_stride, ws.data_ptr(),
+                                       ws.numel(), stream))
     return (o, e) if lse else o
 
 
@@ -625,7 +636,7 @@ def spts_cache_evict(k_pages, v_pages, page_table, seq_lens, weights, keep, sink
                                     weights_out, new_lens, kept, ws)
     cache = _paged(k_pages, v_pages, page_table, seq_lens, dev)
     view, Hkv, d, B, page, max_pages = cache
-    Hs, stride, n = _scores(weights, cache, dev, "weights")
+    Hs, w_stride, n = _scores(weights, cache, dev, "weights")
     if n < max_pages * page:
         raise ValueError("weights: need a slot for every slot of a page table row")
     dst = page_table if dst_table is None else _want(dst_table, _I32, 2, dev, "dst_table")
@@ -640,12 +651,15 @@ def spts_cache_evict(k_pages, v_pages, page_table, seq_lens, weights, keep, sink
     if new_lens is None:
         new_lens = seq_lens.new_empty(B)
     idx = seq_lens.new_empty((B, Hs, keep)) if kept else None
+    dst_stride, lens = _table_stride(dst, "dst_table"), _vector(new_lens, B, dev, "new_lens")
     stream = _raw_stream(dev.index)
+    lock = _issue_lock if ws is None else _no_lock
     ws = _own_ws(ws, lib.spts_cache_evict_workspace(view, Hs, keep), dev, stream)
-    check(lib.spts_cache_evict(C.byref(_bf16_desc(Hkv, Hkv, d)), view, weights.data_ptr(), Hs, stride, keep, sink,
-                               recent, dst.data_ptr(), dst.shape[1], _table_stride(dst, "dst_table"),
-                               weights_out.data_ptr(), out_stride, _vector(new_lens, B, dev, "new_lens"),
-                               None if idx is None else idx.data_ptr(), ws.data_ptr(), ws.numel(), stream))
+    with lock:
+        check(lib.spts_cache_evict(C.byref(_bf16_desc(Hkv, Hkv, d)), view, weights.data_ptr(), Hs, w_stride, keep,
+                                   sink, recent, dst.data_ptr(), dst.shape[1], dst_stride, weights_out.data_ptr(),
+                                   out_stride, lens, None if idx is None else idx.data_ptr(), ws.data_ptr(),
+                                   ws.numel(), stream))
     return (new_lens, weights_out, idx) if kept else (new_lens, weights_out)
 
 
