@@ -370,7 +370,8 @@ SPTS_API spts_status spts_cache_append(const spts_attn_desc *a, const spts_paged
 /* Attention of new tokens over the cache: with n = cu_q[b+1] - cu_q[b] and
  * L = seq_lens[b], query row cu_q[b] + i sees the slots t <= L - n + i of
  * sequence b (its own token, which must be cached already, and all before it;
- * n == 1 is a step of decoding, n == L a whole prompt).
+ * n == 1 is a step of decoding, n == L a whole prompt; with n > L the first
+ * n - L rows see none).
  *   q, o     [T, Hq, d] bf16, rows q_stride / o_stride elements apart
  *            (multiples of 8, 0: Hq * d); o must not overlap q; rows from
  *            cu_q[B] on are not read and left as they are
@@ -380,7 +381,8 @@ SPTS_API spts_status spts_cache_append(const spts_attn_desc *a, const spts_paged
  *   weights  [B, Hs, w_stride] fp32 in/out, or NULL; Hs = Hkv or 1.
  *            weights[b, g, t] += the softmax weight that slot t received,
  *            summed over the sequence's new tokens and the query heads of KV
- *            head g (all query heads with Hs = 1), in a fixed order
+ *            head g (all query heads with Hs = 1), in a fixed order; what the
+ *            additions round away does not grow with the number of tokens
  *            w_stride >= max_pages * page_size; slots from L on are left;
  *            where a row or key is not finite, what its sequence gets is
  *            unspecified
@@ -408,8 +410,10 @@ SPTS_API size_t spts_paged_attention_workspace(const spts_attn_desc *a, const sp
  *   dst_table    [B, dst_max_pages] int32, rows dst_stride entries apart (0:
  *                dst_max_pages), pages of the same k_pages / v_pages with room
  *                for min(seq_lens[b], keep) slots.  Either disjoint from every
- *                page the cache's own table names, or that same pointer:
- *                then the cache is compacted in place
+ *                page the cache's own table names, or that same pointer (with
+ *                any width, and the same row stride if B > 1): then the cache
+ *                is compacted in place.  Rows that move to pages of their own
+ *                sequence through another pointer overwrite one another
  *   weights_out  [B, Hs, w_out_stride] fp32 out, disjoint from weights, or
  *                weights itself; w_out_stride >= min(keep, max_pages *
  *                page_size).  The kept tokens' weights, then zeros to the

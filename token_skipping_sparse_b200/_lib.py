@@ -582,7 +582,9 @@ def spts_paged_attention_workspace(q, k_pages, v_pages, page_table, seq_lens, we
 def spts_paged_attention(q, k_pages, v_pages, page_table, seq_lens, cu_q, scale=None, out=None, lse=False,
                          weights=None, ws=None):
     """Attention of packed new tokens q [T, Hq, d] over the paged cache, causal inside each sequence.
-    Returns o [T, Hq, d], with lse=True (o, lse [T, Hq]); `weights` [B, Hkv or 1, slots] is added to in place."""
+    Returns o [T, Hq, d], with lse=True (o, lse [T, Hq]); `weights` [B, Hkv or 1, slots] is added to in place.
+    How the work is launched goes by the width of page_table, not by the lengths, which are on the device: with
+    weights, pass the columns that are in use (page_table[:, :k])."""
     dev = q.device
     if _elsewhere(dev, "spts_paged_attention"):
         with torch.cuda.device(dev):
@@ -627,8 +629,10 @@ def spts_cache_evict_workspace(k_pages, v_pages, page_table, seq_lens, weights, 
 def spts_cache_evict(k_pages, v_pages, page_table, seq_lens, weights, keep, sink=0, recent=0, dst_table=None,
                      weights_out=None, new_lens=None, kept=False, ws=None):
     """Keeps `keep` tokens of every longer sequence by accumulated weight.  With dst_table the kept rows go to its
-    pages, without it the cache and (unless weights_out is given) the weights are compacted in place.
-    Returns (new_lens, weights_out), with kept=True also the kept slots [B, Hs, keep] (-1 behind the last)."""
+    pages, without it the cache and (unless weights_out is given) the weights are compacted in place, which wants
+    weights with contiguous rows.  dst_table must name none of the pages that page_table names, or start where
+    page_table does (page_table[:, :k]: in place); a copy of page_table is neither, and rows would overwrite one
+    another.  Returns (new_lens, weights_out), with kept=True also the kept slots [B, Hs, keep] (-1 behind the last)."""
     dev = k_pages.device
     if _elsewhere(dev, "spts_cache_evict"):
         with torch.cuda.device(dev):

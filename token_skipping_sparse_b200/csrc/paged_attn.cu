@@ -1165,8 +1165,11 @@ bool few_rows(int B, int64_t T, int G) { return T * G <= 16 * static_cast<int64_
 
 Shape shape_of(int B, int64_t T, int64_t slots, int Hq, int Hkv, int d, int ctas) {
   const int G = Hq / Hkv;
-  // Up to WHOLE_SLOTS slots a unit takes no longer than joining its pieces
-  // would (one row over 517 slots: 10.3 us on the GPU against 13.9).
+  // With tables of up to WHOLE_SLOTS slots units are not cut: windows of prompts
+  // would leave many pieces to join (whole against cut, us per call in a row: 61
+  // prompts of up to 235 tokens 46, 81; one of 1000 24, 40; 8 of 400 to 1000 80,
+  // 107).  Steps would be a tenth faster cut (one row over 517 slots 14.0, 12.8;
+  // 300 rows over up to 1001 135, 121).
   const int whole = slots <= WHOLE_SLOTS;
   // One token per sequence or less on average: steps of decoding.  (Sequences
   // with many tokens come out right, in windows of few.)
