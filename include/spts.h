@@ -381,8 +381,8 @@ SPTS_API spts_status spts_cache_append(const spts_attn_desc *a, const spts_paged
  *   weights  [B, Hs, w_stride] fp32 in/out, or NULL; Hs = Hkv or 1.
  *            weights[b, g, t] += the softmax weight that slot t received,
  *            summed over the sequence's new tokens and the query heads of KV
- *            head g (all query heads with Hs = 1), in a fixed order; what the
- *            additions round away does not grow with the number of tokens
+ *            head g (all query heads with Hs = 1), in a fixed order; what a
+ *            call's additions round away does not grow with its new tokens
  *            w_stride >= max_pages * page_size; slots from L on are left;
  *            where a row or key is not finite, what its sequence gets is
  *            unspecified
